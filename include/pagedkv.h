@@ -59,6 +59,11 @@ extern "C" {
 #define PA_ERR_BAD_BLOCK     6  /* (device status) block id / slot outside pool */
 
 #define PA_DTYPE_F16 0
+#define PA_DTYPE_F32 1       /* probabilities of pa_verify_draft only */
+#define PA_DTYPE_BF16 2      /* probabilities of pa_verify_draft only */
+
+#define PA_TREE_MAX_NODES 64   /* drafted nodes of one sequence, its root included */
+#define PA_TREE_MAX_SEQS 4096  /* sequences of one pa_tree_attention call          */
 
 /* Default split-context partition: a context longer than this many tokens
  * is split into partitions of this size whose partial results are merged. */
@@ -71,7 +76,7 @@ extern "C" {
  *   num_layers        layers whose caches share the block ids (>= 1)
  *   num_heads         attention heads H (>= 1)
  *   head_dim          D: 8, 16, 32, 64, 128 or 256 for the device calls
- *   dtype             PA_DTYPE_F16 (the only one)
+ *   dtype             PA_DTYPE_F16 (the only one a pool takes)
  *   partition_tokens  split-context partition size in tokens; 0 selects
  *                     PA_DEFAULT_PARTITION_TOKENS; otherwise a positive
  *                     multiple of block_size (a value at least as long as
@@ -279,6 +284,33 @@ int pa_alloc_slots_n(pa_pool *pool, int32_t n_seqs, const int32_t *seq_ids,
                      const int32_t *counts, int64_t *slot_mapping_out, int32_t *copies_out,
                      int32_t copies_cap, int32_t *n_copies_out);
 
+/* truncate: each listed sequence keeps its first new_lens[i] tokens (0 to its
+ * token count), for instance after a verification has rejected drafted
+ * tokens.  Blocks past them lose a reference, last one first, as in
+ * pa_seq_free; the slots of kept tokens do not change.  A last block left
+ * partly filled leaves the prefix cache (later appends write into it).  Every
+ * argument is checked before anything changes.  Errors: PA_ERR_NO_SEQ,
+ * PA_ERR_INVALID_ARG (a sequence listed twice, a longer length). */
+int pa_seq_truncate(pa_pool *pool, int32_t n_seqs, const int32_t *seq_ids, const int32_t *new_lens);
+
+/* The block manager's side of moving kept rows to the front of a sequence
+ * (pa_evict_select, then pa_compact_kv on every layer): each listed sequence
+ * shrinks to new_lens[i] tokens, and the call exports what the move needs:
+ *   src_tables_out, src_lens_out  (host, n_seqs x max_blocks int32 padded with
+ *                 -1, n_seqs int32) tables and token counts before the call
+ *   dst_tables_out  (host, n_seqs x max_blocks int32, padded with -1) after it
+ * The first ceil(new_len / B) blocks stay where the sequence alone holds
+ * them (the move is then in place) and are replaced by new ones where they are
+ * shared, so other sequences keep what they see; rewritten blocks leave the
+ * prefix cache.  The other blocks are released as in pa_seq_truncate: what
+ * the move reads from them must be moved before anything else is written to
+ * the pool (the same stream does).  A sequence whose length does not change is
+ * left as it is.  All-or-nothing.  Use one pa_compact_kv per layer and call.
+ * Errors: PA_ERR_NO_SEQ, PA_ERR_OUT_OF_BLOCKS, PA_ERR_INVALID_ARG. */
+int pa_seq_compact(pa_pool *pool, int32_t n_seqs, const int32_t *seq_ids, const int32_t *new_lens,
+                   int32_t max_blocks, int32_t *src_tables_out, int32_t *src_lens_out,
+                   int32_t *dst_tables_out);
+
 /* Export block tables and context lengths for a batch, in the layout the
  * attention kernel reads: tables_out (host, n_seqs x max_blocks int32,
  * row-major) gets each sequence's physical block ids, padded with -1;
@@ -466,6 +498,161 @@ int pa_prefill_step_attention(void *out, const void *q, const void *k_new, const
                               const int32_t *ctx_lens, const int32_t *q_starts, int32_t n_seqs,
                               int32_t max_blocks, int32_t max_q_len, int32_t q_rows, float scale,
                               int32_t *status, const pa_pool_desc *desc, void *stream);
+
+/* ---- drafted tokens --------------------------------------------------------
+ * Speculative decoding over the paged cache (not on the pages): a drafter
+ * proposes tokens after each sequence's last one, as a chain or as a tree of
+ * alternatives; the target model scores all of them in one step, the longest
+ * path that verification accepts stays, and the rest goes.  The nodes of
+ * sequence s are rows q_starts[s] .. q_starts[s+1] - 1 of every per-node array,
+ * at most PA_TREE_MAX_NODES; node 0 is the root, the token decided last, and
+ * node i > 0 was drafted after node parents[row], an earlier node of the
+ * sequence.  One step:
+ *   pa_alloc_slots_n (n nodes a sequence), pa_write_kv and pa_tree_attention in
+ *   every layer, pa_verify_draft on the target's probabilities, pa_compact_kv
+ *   (all layers, keep = path, first = ctx - n) and pa_seq_truncate to
+ *   ctx - n + path_lens[s] tokens; next_tokens[s] is the next step's root. */
+
+/* Attention of each sequence's drafted nodes.  Node i's K/V are stored at
+ * position ctx - n + i (ctx = ctx_lens[s] counts them); it attends to every
+ * position before ctx - n, to itself and to its ancestors:
+ *     out[row][h] = sum_j softmax_j(scale * q[row][h] . k_j) v_j.
+ *   out, q        [q_rows][num_heads][head_dim] fp16, 16-byte aligned like the
+ *                 caches; rows of no sequence are left as they are
+ *   q_starts      [n_seqs + 1] int32, non-decreasing
+ *   parents       [q_rows] int32: -1 (sees only itself among the nodes) or an
+ *                 earlier node of the sequence; NULL: a chain (node i after
+ *                 node i - 1), which is pa_prefill_attention of a short chunk
+ *   max_q_len     host bound on the nodes of a sequence (<= PA_TREE_MAX_NODES)
+ *   workspace     >= pa_tree_workspace_bytes(n_seqs, max_blocks, max_q_len,
+ *                 desc) bytes, 256-byte aligned, uninitialised, of this call
+ *                 alone while it runs
+ * Other arguments as in pa_prefill_attention.  head_dim 64 or 128, block_size
+ * 8, 16 or 32, n_seqs <= PA_TREE_MAX_SEQS.  How long contexts are cut into
+ * parts depends on the whole batch, so a sequence's result agrees between
+ * batches to rounding, not to the bit; it does not depend on where blocks are.
+ * Slots past ctx are never used.  Reported in *status: PA_ERR_INVALID_ARG for
+ * n < 0, n > ctx, n > max_q_len or rows outside [0, q_rows) (that sequence is
+ * left unwritten), and for a parent that is no earlier node (taken as -1);
+ * PA_ERR_BAD_BLOCK for ctx > max_blocks * B (left unwritten) or a table entry
+ * outside the pool (not read; the sequence's output is unspecified).
+ * pa_tree_workspace_bytes is 0 where the call would be refused.
+ * Errors: PA_ERR_INVALID_ARG, PA_ERR_CUDA. */
+size_t pa_tree_workspace_bytes(int32_t n_seqs, int32_t max_blocks, int32_t max_q_len,
+                               const pa_pool_desc *desc);
+int pa_tree_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
+                      const int32_t *block_tables, const int32_t *ctx_lens, const int32_t *q_starts,
+                      const int32_t *parents, int32_t n_seqs, int32_t max_blocks, int32_t max_q_len,
+                      int32_t q_rows, float scale, void *workspace, size_t workspace_bytes,
+                      int32_t *status, const pa_pool_desc *desc, void *stream);
+
+/* Verification of drafted nodes from given uniform numbers, so that the
+ * tokens kept are distributed as the target's own samples.  From the root on,
+ * at node v with target probabilities p = target_probs[row of v] and draft
+ * probabilities q = draft_probs[row of v], w = p and Z = 1 at first, the
+ * children c of v in index order, with token x = draft_tokens[row of c]:
+ *     accepted if u_accept[row of c] * q(x) * Z < w(x): the walk goes on at c;
+ *     otherwise w = max(w - Z q, 0) and Z = sum w (both unchanged where that
+ *     sum is 0).
+ * Where no child is accepted, next_tokens[s] is the first i whose running sum
+ * of w passes u_sample[s] * sum w (the last i of positive weight where
+ * rounding leaves none), so the call also samples where there is no draft.
+ * Evaluated to 2^-48 or better.
+ *   path          [n_seqs][max_q_len] int32, out: the accepted nodes, the root
+ *                 (0) first, ascending, padded with -1
+ *   path_lens     [n_seqs] int32, out: how many (>= 1)
+ *   next_tokens   [n_seqs] int32, out
+ *   target_probs, draft_probs  [q_rows][vocab] of dtype (PA_DTYPE_F32, _F16 or
+ *                 _BF16), row of node v: the distribution of the token after
+ *                 v.  Entries that are not positive and finite count as 0;
+ *                 rows are taken to sum to 1.  draft_probs NULL: each drafted
+ *                 token was picked outright (q is 1 at x).
+ *   draft_tokens  [q_rows] int32 (the root's entry is not read)
+ *   parents       [q_rows] int32 as above (the root's entry is not read; a
+ *                 node with parent -1 is not reached); NULL: a chain
+ *   u_accept      [q_rows] fp32 in [0, 1) (the root's entry is not used)
+ *   u_sample      [n_seqs] fp32 in [0, 1)
+ * A sequence of no nodes gets path_lens 0 and next_tokens -1.  Reported in
+ * *status as PA_ERR_INVALID_ARG: rows outside [0, q_rows) or n > max_q_len
+ * (path_lens 0, next_tokens -1), a parent that is no earlier node or a token
+ * outside the vocabulary (the node is not reached), a row without any positive
+ * weight to sample from (next_tokens -1).
+ * Errors: PA_ERR_INVALID_ARG, PA_ERR_CUDA. */
+int pa_verify_draft(int32_t *path, int32_t *path_lens, int32_t *next_tokens,
+                    const void *target_probs, const void *draft_probs, int32_t dtype,
+                    const int32_t *draft_tokens, const int32_t *parents, const int32_t *q_starts,
+                    const float *u_accept, const float *u_sample, int32_t n_seqs, int32_t max_q_len,
+                    int32_t q_rows, int32_t vocab, int32_t *status, void *stream);
+
+/* ---- a bounded cache ---------------------------------------------------------
+ * Eviction by accumulated attention weight (not on the pages): decode steps
+ * add up the weight each cached position receives, per (sequence, head); when a
+ * sequence is over its budget the positions with the largest sums and the
+ * most recent ones stay, per head, and move to its front:
+ *   pa_decode_attention_weights in every layer of every step;
+ *   pa_seq_compact (host), then pa_evict_select and pa_compact_kv per layer.
+ * (Keys keep the position encoding they were stored with.) */
+
+/* pa_decode_attention (same arguments and meaning, its own workspace) that
+ * also gives every cached position's weight,
+ *     weights_out[s][h][p] = weights_in[s][h][p] + softmax_p(scale * q . k_p),
+ * p < ctx.  weights_out, weights_in: [n_seqs][num_heads][weight_len] fp32, the
+ * same buffer or disjoint ones; weights_in NULL counts as 0; entries from ctx on
+ * are neither read nor written.  head_dim 64 or 128, block_size 8, 16 or 32,
+ * n_seqs <= PA_TREE_MAX_SEQS.  A context above weight_len is reported as
+ * PA_ERR_INVALID_ARG, one above max_blocks * B as PA_ERR_BAD_BLOCK, and that
+ * sequence left unwritten; ctx <= 0 gives o = 0.  The workspace holds a
+ * score per (sequence, head, slot) beside what cut contexts need; its size is 0
+ * where the call would be refused.  Parts and rounding as in pa_tree_attention.
+ * Errors: PA_ERR_INVALID_ARG, PA_ERR_CUDA. */
+size_t pa_decode_weights_workspace_bytes(int32_t n_seqs, int32_t max_blocks, const pa_pool_desc *desc);
+int pa_decode_attention_weights(void *out, float *weights_out, const float *weights_in,
+                                int32_t weight_len, const void *q, const void *k_cache,
+                                const void *v_cache, const int32_t *block_tables,
+                                const int32_t *ctx_lens, int32_t n_seqs, int32_t max_blocks,
+                                float scale, void *workspace, size_t workspace_bytes,
+                                int32_t *status, const pa_pool_desc *desc, void *stream);
+
+/* Which positions of each (sequence, head) stay: all where ctx <= budget,
+ * otherwise the last `recent` (0 to budget) and the budget - recent others with
+ * the largest weights_in (ties to the lowest position; NaN below every
+ * number).
+ *   keep          [n_seqs][num_heads][budget] int32, out: ascending, padded -1
+ *   keep_lens     [n_seqs] int32, out: min(ctx, budget)
+ *   weights_out, weights_in  [n_seqs][num_heads][weight_len] fp32, the same
+ *                 buffer or disjoint ones: weights_out[j] = weights_in[keep[j]]
+ *                 for j < keep_len, 0 from there to ctx; the rest is not touched
+ * A ctx above weight_len is reported as PA_ERR_INVALID_ARG (keep_len 0, weights
+ * left as they are).  Errors: PA_ERR_INVALID_ARG, PA_ERR_CUDA. */
+int pa_evict_select(int32_t *keep, int32_t *keep_lens, float *weights_out, const float *weights_in,
+                    int32_t weight_len, const int32_t *ctx_lens, int32_t n_seqs, int32_t num_heads,
+                    int32_t budget, int32_t recent, int32_t *status, void *stream);
+
+/* Move kept rows: for every layer, sequence s, head h and j < keep_lens[s],
+ * the K/V row at position first + j (through dst_tables) becomes the one that
+ * was at position first + keep[s][h][j] (through src_tables), first = first[s].
+ * keep must be strictly ascending, so the move works in place; dst_tables may
+ * be src_tables, or hold, entry by entry, either the same block or one that
+ * src_tables does not hold anywhere in the call (pa_seq_compact's).  Two
+ * sequences must not write one block.
+ *   k_caches, v_caches  (host) arrays of num_layers (<= 128) device pointers
+ *   src_tables, dst_tables  [n_seqs][max_blocks] int32
+ *   src_lens      [n_seqs] int32: positions the sequence holds before the move
+ *   first         [n_seqs] int32, or NULL for 0
+ *   keep          [n_seqs][keep_heads][keep_stride] int32, keep_heads 1 (one
+ *                 list for all heads) or num_heads; entries from keep_lens[s] on
+ *                 are not read
+ *   keep_lens     [n_seqs] int32, <= keep_stride; <= 0 moves nothing
+ * Reported in *status, the row (or, for a bad keep_lens or first, the sequence)
+ * not moved: PA_ERR_INVALID_ARG for a keep entry that does not ascend or lies
+ * outside the sequence, PA_ERR_BAD_BLOCK for a position past max_blocks * B or
+ * a table entry outside the pool.  Any geometry of the device calls.
+ * Errors: PA_ERR_INVALID_ARG, PA_ERR_CUDA. */
+int pa_compact_kv(void *const *k_caches, void *const *v_caches, int32_t num_layers,
+                  const int32_t *src_tables, const int32_t *dst_tables, const int32_t *src_lens,
+                  const int32_t *first, const int32_t *keep, const int32_t *keep_lens,
+                  int32_t keep_heads, int32_t keep_stride, int32_t n_seqs, int32_t max_blocks,
+                  const pa_pool_desc *desc, int32_t *status, void *stream);
 
 /* ---- decode attention without a caller-provided workspace ------------------
  * No counterpart on the pages: this entry point exists for callers that

@@ -27,6 +27,10 @@ PA_ERR_CUDA = 4
 PA_ERR_TIMEOUT = 5
 PA_ERR_BAD_BLOCK = 6
 PA_DTYPE_F16 = 0
+PA_DTYPE_F32 = 1
+PA_DTYPE_BF16 = 2
+PA_TREE_MAX_NODES = 64
+PA_TREE_MAX_SEQS = 4096
 PA_POOL_PREFIX_CACHING = 1
 PA_DEFAULT_PARTITION_TOKENS = 512
 PA_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -105,6 +109,19 @@ def _load():
                                        ctypes.c_float, vp, P(pa_pool_desc), vp]),
         "pa_prefill_step_attention": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32,
                                             i32, ctypes.c_float, vp, P(pa_pool_desc), vp]),
+        "pa_seq_truncate": (i32, [vp, i32, vp, vp]),
+        "pa_seq_compact": (i32, [vp, i32, vp, vp, i32, vp, vp, vp]),
+        "pa_tree_workspace_bytes": (sz, [i32, i32, i32, P(pa_pool_desc)]),
+        "pa_tree_attention": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                    ctypes.c_float, vp, sz, vp, P(pa_pool_desc), vp]),
+        "pa_verify_draft": (i32, [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                  vp, vp]),
+        "pa_decode_weights_workspace_bytes": (sz, [i32, i32, P(pa_pool_desc)]),
+        "pa_decode_attention_weights": (i32, [vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32,
+                                              ctypes.c_float, vp, sz, vp, P(pa_pool_desc), vp]),
+        "pa_evict_select": (i32, [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, vp, vp]),
+        "pa_compact_kv": (i32, [vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                P(pa_pool_desc), vp, vp]),
         "pa_selftest_bounded_wait": (i32, [vp, vp]),
     }
     for name, (res, args) in sig.items():
@@ -132,9 +149,10 @@ def _check(rc: int):
 
 def _need_elems(n_elems: int, **tensors):
     """Refuses a tensor holding fewer elements than the call reads from it
-    (None is left to the library, which refuses a NULL it needs)."""
+    (None is left to the library, which refuses a NULL it needs; a raw address
+    has no length to check)."""
     for name, t in tensors.items():
-        if t is not None and t.numel() < n_elems:
+        if t is not None and not isinstance(t, int) and t.numel() < n_elems:
             raise ValueError(f"{name} holds {t.numel()} elements, the call reads {n_elems}")
 
 
@@ -432,6 +450,29 @@ def pa_pool_refcounts(pool, num_blocks: int):
     return out[: int(num_blocks)]
 
 
+def pa_seq_truncate(pool, seq_ids, new_lens) -> None:
+    """Each sequence keeps its first new_lens[i] tokens; blocks past them are released."""
+    ids, lens = _host_i32(seq_ids), _host_i32(new_lens)
+    if ids.shape != lens.shape:
+        raise ValueError("seq_ids and new_lens differ in length")
+    _check(_lib.pa_seq_truncate(pool, ids.shape[0], ids.ctypes.data, lens.ctypes.data))
+
+
+def pa_seq_compact(pool, seq_ids, new_lens, max_blocks: int):
+    """Shrinks the sequences to new_lens tokens whose rows pa_compact_kv moves to
+    their front.  Returns (src_tables int32[n, max_blocks], src_lens int32[n],
+    dst_tables int32[n, max_blocks]), tables padded with -1."""
+    ids, lens = _host_i32(seq_ids), _host_i32(new_lens)
+    if ids.shape != lens.shape:
+        raise ValueError("seq_ids and new_lens differ in length")
+    n = ids.shape[0]
+    src, dst = np.empty((n, max_blocks), np.int32), np.empty((n, max_blocks), np.int32)
+    src_lens = np.empty(n, np.int32)
+    _check(_lib.pa_seq_compact(pool, n, ids.ctypes.data, lens.ctypes.data, int(max_blocks),
+                               src.ctypes.data, src_lens.ctypes.data, dst.ctypes.data))
+    return src, src_lens, dst
+
+
 # -------------------------------------------------------------- device calls
 def pa_write_kv(k, v, slot_mapping, k_cache, v_cache, desc: PoolDesc, status=None,
                 stream=None, n_tokens: int | None = None) -> None:
@@ -516,6 +557,155 @@ def pa_prefill_step_attention(out, q, k_new, v_new, k_cache, v_cache, block_tabl
                                           _dev(ctx_lens), _dev(q_starts), n, mb, int(max_q_len),
                                           rows, ctypes.c_float(scale), _dev(status), desc.ref,
                                           _stream(stream)))
+
+
+def _need_dtype(kind: str, **tensors):
+    """Refuses a tensor whose element type is not the one the call reads."""
+    for name, t in tensors.items():
+        if t is not None and not isinstance(t, int) and str(t.dtype) != "torch." + kind:
+            raise ValueError(f"{name} is {t.dtype}, the call reads {kind}")
+
+
+def pa_tree_workspace_bytes(n_seqs: int, max_blocks: int, max_q_len: int, desc: PoolDesc) -> int:
+    return int(_lib.pa_tree_workspace_bytes(int(n_seqs), int(max_blocks), int(max_q_len), desc.ref))
+
+
+def pa_tree_attention(out, q, k_cache, v_cache, block_tables, ctx_lens, q_starts, parents,
+                      scale: float, desc: PoolDesc, max_q_len: int, workspace=None, status=None,
+                      stream=None, n_seqs: int | None = None, max_blocks: int | None = None,
+                      q_rows: int | None = None) -> None:
+    """Attention of drafted nodes: rows q_starts[s]..q_starts[s+1]-1 of q are
+    the last positions of sequence s, each seeing the positions before the
+    nodes, itself and its ancestors by ``parents`` (None: a chain)."""
+    n = int(ctx_lens.shape[0]) if n_seqs is None else int(n_seqs)
+    mb = int(block_tables.shape[1]) if max_blocks is None else int(max_blocks)
+    rows = min(int(q.shape[0]), int(out.shape[0])) if q_rows is None else int(q_rows)
+    _need_dtype("float16", out=out, q=q, k_cache=k_cache, v_cache=v_cache)
+    _need_dtype("int32", block_tables=block_tables, ctx_lens=ctx_lens, q_starts=q_starts,
+                parents=parents)
+    _need_elems(rows * desc.num_heads * desc.head_dim, q=q, out=out)
+    _need_elems(n, ctx_lens=ctx_lens)
+    _need_elems(n + 1, q_starts=q_starts)
+    _need_elems(n * mb, block_tables=block_tables)
+    _need_elems(rows, parents=parents)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.pa_tree_attention(_dev(out), _dev(q), _dev(k_cache), _dev(v_cache),
+                                  _dev(block_tables), _dev(ctx_lens), _dev(q_starts),
+                                  _dev(parents), n, mb, int(max_q_len), rows,
+                                  ctypes.c_float(scale), _dev(workspace), ws_bytes, _dev(status),
+                                  desc.ref, _stream(stream)))
+
+
+_PROB_DTYPES = {"torch.float32": PA_DTYPE_F32, "torch.float16": PA_DTYPE_F16,
+                "torch.bfloat16": PA_DTYPE_BF16}
+
+
+def pa_verify_draft(path, path_lens, next_tokens, target_probs, draft_probs, draft_tokens,
+                    parents, q_starts, u_accept, u_sample, max_q_len: int | None = None,
+                    status=None, stream=None, n_seqs: int | None = None) -> None:
+    """Accepted path, its length and the next token of every sequence from the
+    target's and the drafter's probabilities ([rows, vocab]; draft_probs None:
+    tokens picked outright) and given uniform numbers.  ``path`` is
+    int32 [n_seqs, max_q_len]."""
+    n = int(u_sample.shape[0]) if n_seqs is None else int(n_seqs)
+    mq = int(path.shape[1]) if max_q_len is None else int(max_q_len)
+    rows, vocab = (int(x) for x in target_probs.shape)
+    kind = str(target_probs.dtype)
+    if kind not in _PROB_DTYPES:
+        raise ValueError(f"target_probs is {kind}: float32, float16 or bfloat16 expected")
+    _need_dtype(kind[6:], draft_probs=draft_probs)
+    _need_dtype("int32", path=path, path_lens=path_lens, next_tokens=next_tokens,
+                draft_tokens=draft_tokens, parents=parents, q_starts=q_starts)
+    _need_dtype("float32", u_accept=u_accept, u_sample=u_sample)
+    _need_elems(rows * vocab, draft_probs=draft_probs)
+    _need_elems(rows, draft_tokens=draft_tokens, parents=parents, u_accept=u_accept)
+    _need_elems(n, path_lens=path_lens, next_tokens=next_tokens, u_sample=u_sample)
+    _need_elems(n + 1, q_starts=q_starts)
+    _need_elems(n * mq, path=path)
+    _check(_lib.pa_verify_draft(_dev(path), _dev(path_lens), _dev(next_tokens), _dev(target_probs),
+                                _dev(draft_probs), _PROB_DTYPES[kind], _dev(draft_tokens),
+                                _dev(parents), _dev(q_starts), _dev(u_accept), _dev(u_sample), n, mq,
+                                rows, vocab, _dev(status), _stream(stream)))
+
+
+def pa_decode_weights_workspace_bytes(n_seqs: int, max_blocks: int, desc: PoolDesc) -> int:
+    return int(_lib.pa_decode_weights_workspace_bytes(int(n_seqs), int(max_blocks), desc.ref))
+
+
+def pa_decode_attention_weights(out, weights_out, weights_in, q, k_cache, v_cache, block_tables,
+                                ctx_lens, scale: float, desc: PoolDesc, workspace=None,
+                                status=None, stream=None, n_seqs: int | None = None,
+                                max_blocks: int | None = None) -> None:
+    """pa_decode_attention that adds each position's weight to weights_in
+    (float32 [n_seqs, num_heads, weight_len], None: zeros) into weights_out,
+    which may be the same tensor."""
+    n = int(q.shape[0]) if n_seqs is None else int(n_seqs)
+    mb = int(block_tables.shape[1]) if max_blocks is None else int(max_blocks)
+    wl = int(weights_out.shape[-1])
+    _need_dtype("float16", out=out, q=q, k_cache=k_cache, v_cache=v_cache)
+    _need_dtype("float32", weights_out=weights_out, weights_in=weights_in)
+    _need_dtype("int32", block_tables=block_tables, ctx_lens=ctx_lens)
+    _need_elems(n * desc.num_heads * desc.head_dim, q=q, out=out)
+    _need_elems(n * desc.num_heads * wl, weights_out=weights_out, weights_in=weights_in)
+    _need_elems(n, ctx_lens=ctx_lens)
+    _need_elems(n * mb, block_tables=block_tables)
+    if weights_in is not None and int(weights_in.shape[-1]) != wl:
+        raise ValueError("weights_in and weights_out differ in length")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.pa_decode_attention_weights(_dev(out), _dev(weights_out), _dev(weights_in), wl,
+                                            _dev(q), _dev(k_cache), _dev(v_cache),
+                                            _dev(block_tables), _dev(ctx_lens), n, mb,
+                                            ctypes.c_float(scale), _dev(workspace), ws_bytes,
+                                            _dev(status), desc.ref, _stream(stream)))
+
+
+def pa_evict_select(keep, keep_lens, weights_out, weights_in, ctx_lens, budget: int, recent: int,
+                    status=None, stream=None, n_seqs: int | None = None) -> None:
+    """Positions that stay, per (sequence, head): the last ``recent`` and those
+    with the largest weights_in, ``budget`` in all, into keep (int32
+    [n_seqs, num_heads, budget], ascending, padded with -1); their weights into
+    weights_out, which may be weights_in."""
+    n = int(ctx_lens.shape[0]) if n_seqs is None else int(n_seqs)
+    heads, wl = int(weights_in.shape[1]), int(weights_in.shape[2])
+    if tuple(weights_out.shape[1:]) != (heads, wl):
+        raise ValueError("weights_in and weights_out differ in shape")
+    _need_dtype("int32", keep=keep, keep_lens=keep_lens, ctx_lens=ctx_lens)
+    _need_dtype("float32", weights_out=weights_out, weights_in=weights_in)
+    _need_elems(n * heads * max(int(budget), 0), keep=keep)
+    _need_elems(n * heads * wl, weights_out=weights_out, weights_in=weights_in)
+    _need_elems(n, keep_lens=keep_lens, ctx_lens=ctx_lens)
+    _check(_lib.pa_evict_select(_dev(keep), _dev(keep_lens), _dev(weights_out), _dev(weights_in), wl,
+                                _dev(ctx_lens), n, heads, int(budget), int(recent), _dev(status),
+                                _stream(stream)))
+
+
+def pa_compact_kv(k_caches, v_caches, src_tables, dst_tables, src_lens, keep, keep_lens,
+                  desc: PoolDesc, first=None, status=None, stream=None,
+                  n_seqs: int | None = None) -> None:
+    """Every layer's K/V rows at positions first + keep[s, h, j] (src_tables)
+    move to first + j (dst_tables).  keep: int32 [n_seqs, 1 or num_heads, n]
+    or [n_seqs, n] (one list for all heads)."""
+    L = len(k_caches)
+    n = int(keep_lens.shape[0]) if n_seqs is None else int(n_seqs)
+    mb = int(src_tables.shape[1])
+    heads = int(keep.shape[1]) if keep.dim() == 3 else 1
+    stride = int(keep.shape[-1])
+    if len(v_caches) != L:
+        raise ValueError("k_caches and v_caches differ in length")
+    if int(dst_tables.shape[1]) != mb:
+        raise ValueError("src_tables and dst_tables differ in width")
+    for cache in (*k_caches, *v_caches):
+        _need_dtype("float16", cache=cache)
+    _need_dtype("int32", src_tables=src_tables, dst_tables=dst_tables, src_lens=src_lens,
+                keep=keep, keep_lens=keep_lens, first=first)
+    _need_elems(n * mb, src_tables=src_tables, dst_tables=dst_tables)
+    _need_elems(n, src_lens=src_lens, keep_lens=keep_lens, first=first)
+    _need_elems(n * heads * stride, keep=keep)
+    kp = (ctypes.c_void_p * L)(*[_dev(x) for x in k_caches])
+    vp = (ctypes.c_void_p * L)(*[_dev(x) for x in v_caches])
+    _check(_lib.pa_compact_kv(kp, vp, L, _dev(src_tables), _dev(dst_tables), _dev(src_lens),
+                              _dev(first), _dev(keep), _dev(keep_lens), heads, stride, n, mb,
+                              desc.ref, _dev(status), _stream(stream)))
 
 
 def pa_selftest_bounded_wait(status, stream=None) -> None:

@@ -135,4 +135,57 @@ int pa_prefill_attention(void *out, const void *q, const void *k_cache, const vo
                                     stream);
 }
 
+size_t pa_tree_workspace_bytes(int32_t n_seqs, int32_t max_blocks, int32_t max_q_len,
+                               const pa_pool_desc *desc) {
+    return tree_workspace_bytes(n_seqs, max_blocks, max_q_len, desc);
+}
+
+int pa_tree_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
+                      const int32_t *block_tables, const int32_t *ctx_lens, const int32_t *q_starts,
+                      const int32_t *parents, int32_t n_seqs, int32_t max_blocks, int32_t max_q_len,
+                      int32_t q_rows, float scale, void *workspace, size_t workspace_bytes,
+                      int32_t *status, const pa_pool_desc *desc, void *stream) {
+    return launch_tree_attention(out, q, k_cache, v_cache, block_tables, ctx_lens, q_starts, parents, n_seqs,
+                                 max_blocks, max_q_len, q_rows, scale, workspace, workspace_bytes, status, desc,
+                                 stream);
+}
+
+int pa_verify_draft(int32_t *path, int32_t *path_lens, int32_t *next_tokens, const void *target_probs,
+                    const void *draft_probs, int32_t dtype, const int32_t *draft_tokens, const int32_t *parents,
+                    const int32_t *q_starts, const float *u_accept, const float *u_sample, int32_t n_seqs,
+                    int32_t max_q_len, int32_t q_rows, int32_t vocab, int32_t *status, void *stream) {
+    return launch_verify_draft(path, path_lens, next_tokens, target_probs, draft_probs, dtype, draft_tokens,
+                               parents, q_starts, u_accept, u_sample, n_seqs, max_q_len, q_rows, vocab, status,
+                               stream);
+}
+
+size_t pa_decode_weights_workspace_bytes(int32_t n_seqs, int32_t max_blocks, const pa_pool_desc *desc) {
+    return decode_weights_workspace_bytes(n_seqs, max_blocks, desc);
+}
+
+int pa_decode_attention_weights(void *out, float *weights_out, const float *weights_in, int32_t weight_len,
+                                const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *block_tables, const int32_t *ctx_lens, int32_t n_seqs,
+                                int32_t max_blocks, float scale, void *workspace, size_t workspace_bytes,
+                                int32_t *status, const pa_pool_desc *desc, void *stream) {
+    return launch_decode_attention_weights(out, weights_out, weights_in, weight_len, q, k_cache, v_cache,
+                                           block_tables, ctx_lens, n_seqs, max_blocks, scale, workspace,
+                                           workspace_bytes, status, desc, stream);
+}
+
+int pa_evict_select(int32_t *keep, int32_t *keep_lens, float *weights_out, const float *weights_in,
+                    int32_t weight_len, const int32_t *ctx_lens, int32_t n_seqs, int32_t num_heads,
+                    int32_t budget, int32_t recent, int32_t *status, void *stream) {
+    return launch_evict_select(keep, keep_lens, weights_out, weights_in, weight_len, ctx_lens, n_seqs, num_heads,
+                               budget, recent, status, stream);
+}
+
+int pa_compact_kv(void *const *k_caches, void *const *v_caches, int32_t num_layers, const int32_t *src_tables,
+                  const int32_t *dst_tables, const int32_t *src_lens, const int32_t *first, const int32_t *keep,
+                  const int32_t *keep_lens, int32_t keep_heads, int32_t keep_stride, int32_t n_seqs,
+                  int32_t max_blocks, const pa_pool_desc *desc, int32_t *status, void *stream) {
+    return launch_compact_kv(k_caches, v_caches, num_layers, src_tables, dst_tables, src_lens, first, keep,
+                             keep_lens, keep_heads, keep_stride, n_seqs, max_blocks, desc, status, stream);
+}
+
 }  // extern "C"

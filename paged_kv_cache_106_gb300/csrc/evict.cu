@@ -1,0 +1,389 @@
+// Keeping part of a cached context: which positions a budget keeps by the
+// attention weight they have accumulated (pa_evict_select), and moving kept
+// rows of the cache to the front of their sequence (pa_compact_kv), which is
+// also how accepted drafts get into place after a verification.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pagedkv {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+// ---------------------------------------------------------------- selection
+//
+// For one (sequence, head): the last `recent` of ctx positions and, of the
+// others, the budget - recent with the largest sums (ties to the lowest
+// position), in ascending order.  One CTA finds the sum of the last one kept
+// by radix selection on order-preserving keys, 11 + 11 + 10 bits (the first
+// digit holds sign, exponent and 2 mantissa bits, so the sums of one head
+// spread over many bins and the shared-memory counters do not queue up), then
+// writes the kept positions in order with one counting and one writing sweep,
+// each warp over a contiguous span.  It reads 4 bytes a position from memory
+// once: contexts up to kCached positions stay in shared memory, longer ones
+// are re-read through L2.
+
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kCached = 24576;       // positions of a row kept in shared memory (96 KB)
+
+// Larger sums have larger keys; -0 counts as 0, NaN as less than everything.
+__device__ __forceinline__ uint32_t key_of(float x) {
+    if (x != x) return 0u;
+    const uint32_t b = __float_as_uint(x == 0.f ? 0.f : x);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+struct SelectParams {
+    int32_t *keep, *keep_lens;
+    float *w_out;
+    const float *w_in;
+    const int32_t *ctx_lens;
+    int32_t weight_len, budget, recent, num_heads;
+    int32_t *status;
+};
+
+template <bool CACHED>
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams a) {
+    extern __shared__ float row_sh[];
+    __shared__ uint32_t bins[kBins];
+    __shared__ uint32_t part[kSelWarps], part2[kSelWarps];
+    __shared__ uint32_t found[2];      // digit, and how many of it are still wanted
+    const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ctx = max(a.ctx_lens[s], 0), budget = a.budget;
+    const size_t sh_row = (size_t)s * a.num_heads + h;
+    int32_t *keep = a.keep + sh_row * budget;
+    const float *w = a.w_in + sh_row * a.weight_len;
+    float *wo = a.w_out + sh_row * a.weight_len;
+    const bool bad = ctx > a.weight_len;
+    const int len = bad ? 0 : min(ctx, budget);
+    if (h == 0 && tid == 0) {
+        a.keep_lens[s] = len;
+        if (bad) report(a.status, PA_ERR_INVALID_ARG);
+    }
+    for (int j = len + tid; j < budget; j += kSelThreads) keep[j] = -1;
+    if (bad) return;
+    if (ctx <= budget) {               // everything stays
+        for (int j = tid; j < ctx; j += kSelThreads) {
+            keep[j] = j;
+            wo[j] = w[j];
+        }
+        return;
+    }
+    const int old = ctx - a.recent, heavy = budget - a.recent;   // 0 <= heavy < old
+    if (CACHED) {
+        for (int j = tid; j < ctx; j += kSelThreads) row_sh[j] = w[j];
+        __syncthreads();
+    }
+    auto at = [&](int j) { return CACHED ? row_sh[j] : w[j]; };
+
+    // ---- the key of the last kept position, and how many of that key are kept
+    uint32_t prefix = 0, mask = 0;
+    int want = heavy;
+    if (heavy > 0) {
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const int nb = pass == 2 ? 1024 : 2048;
+            for (int b = tid; b < nb; b += kSelThreads) bins[b] = 0;
+            __syncthreads();
+            for (int j = tid; j < old; j += kSelThreads) {
+                const uint32_t key = key_of(at(j));
+                if ((key & mask) == prefix) atomicAdd(&bins[(key >> shift) & (nb - 1)], 1u);
+            }
+            __syncthreads();
+            // bins from the top: thread t owns the bins [nb - (t+1) e, nb - t e)
+            const int e = nb / kSelThreads;
+            uint32_t mine = 0;
+            for (int k = 0; k < e; ++k) mine += bins[nb - 1 - (tid * e + k)];
+            uint32_t incl = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t y = __shfl_up_sync(kAll, incl, off);
+                if (lane >= off) incl += y;
+            }
+            if (lane == 31) part[warp] = incl;
+            __syncthreads();
+            uint32_t before = incl - mine;
+            for (int k = 0; k < warp; ++k) before += part[k];
+            if ((int)before < want && (int)(before + mine) >= want) {
+                uint32_t run = before;
+                for (int k = 0; k < e; ++k) {
+                    const int b = nb - 1 - (tid * e + k);
+                    if ((int)(run + bins[b]) >= want) {
+                        found[0] = (uint32_t)b;
+                        found[1] = (uint32_t)want - run;
+                        break;
+                    }
+                    run += bins[b];
+                }
+            }
+            __syncthreads();
+            prefix |= found[0] << shift;
+            mask |= (uint32_t)(nb - 1) << shift;
+            want = (int)found[1];
+            __syncthreads();
+        }
+    }
+    const uint32_t last = prefix;
+
+    // ---- kept positions in order: count by warp, then write
+    const int per = (old + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
+    const int lo = min(old, warp * per), hi = min(old, lo + per);
+    uint32_t more = 0, same = 0;
+    if (heavy > 0) {
+        for (int j0 = lo; j0 < hi; j0 += 32) {
+            const int j = j0 + lane;
+            const uint32_t key = j < hi ? key_of(at(j)) : 0u;
+            more += __popc(__ballot_sync(kAll, j < hi && key > last));
+            same += __popc(__ballot_sync(kAll, j < hi && key == last));
+        }
+    }
+    if (lane == 0) {
+        part[warp] = more;
+        part2[warp] = same;
+    }
+    __syncthreads();
+    uint32_t same_run = 0, out = 0;
+    for (int k = 0; k < warp; ++k) {
+        const uint32_t left = (uint32_t)want > same_run ? (uint32_t)want - same_run : 0u;
+        out += part[k] + min(part2[k], left);
+        same_run += part2[k];
+    }
+    if (heavy > 0) {
+        for (int j0 = lo; j0 < hi; j0 += 32) {
+            const int j = j0 + lane;
+            const uint32_t key = j < hi ? key_of(at(j)) : 0u;
+            const unsigned eq = __ballot_sync(kAll, j < hi && key == last);
+            const bool tie = j < hi && key == last &&
+                             same_run + __popc(eq & ((1u << lane) - 1)) < (uint32_t)want;
+            const bool take = (j < hi && key > last) || tie;
+            const unsigned m = __ballot_sync(kAll, take);
+            if (take) {
+                const uint32_t o = out + __popc(m & ((1u << lane) - 1));
+                keep[o] = j;
+                if (CACHED) wo[o] = row_sh[j];
+            }
+            out += __popc(m);
+            same_run += __popc(eq);
+        }
+    }
+    for (int j = tid; j < a.recent; j += kSelThreads) {
+        keep[heavy + j] = old + j;
+        if (CACHED) wo[heavy + j] = row_sh[old + j];
+    }
+    if (!CACHED) {
+        // kept sums move down in ascending order, so each chunk is read before
+        // anything at or after it is written (the two rows may be one)
+        __syncthreads();
+        for (int j0 = 0; j0 < len; j0 += kSelThreads) {
+            const int j = j0 + tid;
+            const float x = j < len ? w[keep[j]] : 0.f;
+            __syncthreads();
+            if (j < len) wo[j] = x;
+            __syncthreads();
+        }
+    }
+    for (int j = len + tid; j < ctx; j += kSelThreads) wo[j] = 0.f;
+}
+
+// ---------------------------------------------------------------- compaction
+//
+// Row j of a sequence's part from position first on becomes the row that was
+// at position first + keep[j], keep strictly ascending: keep[j] >= j, so in
+// place every row is read before anything is written over it as long as reads
+// run ahead of writes in order.  A CTA owns whole columns (16-byte vectors of
+// a head's rows) and walks the rows in chunks: all loads of a chunk, a
+// barrier, all its stores.  Bound by the bytes: each kept row is read and
+// written once; rows already in place are skipped.
+
+constexpr int kMoveThreads = 256, kUnroll = 8;
+constexpr int kMaxMoveLayers = 128;
+constexpr int kMaxChunk = 512;       // rows of a chunk
+
+struct CompactParams {
+    const int32_t *src_tables, *dst_tables, *src_lens, *first, *keep, *keep_lens;
+    int32_t num_heads, keep_heads, keep_stride, max_blocks, num_blocks, bshift, row_shift;
+    int32_t cols, rows, chunk;       // columns and rows a pass of the CTA covers; rows of a chunk
+    int32_t *status;
+    uint4 *cache[2 * kMaxMoveLayers];
+};
+
+__global__ void __launch_bounds__(kMoveThreads) compact_kv_kernel(const __grid_constant__ CompactParams a) {
+    __shared__ long long from[2][kMaxChunk], to[2][kMaxChunk];   // row numbers in the cache, -1: none
+    const int s = blockIdx.y, tid = threadIdx.x;
+    // blockIdx.x: (head of the keep list, group of columns)
+    const int vec = 1 << a.row_shift;                   // vectors of a row
+    const int heads_each = a.num_heads / a.keep_heads;  // heads that share a list: 1 or all
+    const int col_groups = (heads_each * vec + a.cols - 1) / a.cols;
+    const int kh = blockIdx.x / col_groups, cg = blockIdx.x - kh * col_groups;
+    uint4 *cache = a.cache[blockIdx.z];
+    const int len = a.keep_lens[s], ctx = a.src_lens[s], first = a.first ? a.first[s] : 0;
+    const bool tell = tid == 0 && blockIdx.x == 0 && blockIdx.z == 0;
+    if (len <= 0) return;
+    if (len > a.keep_stride || first < 0) {
+        if (tell) report(a.status, PA_ERR_INVALID_ARG);
+        return;
+    }
+    const int32_t *keep = a.keep + ((size_t)s * a.keep_heads + kh) * a.keep_stride;
+    const int32_t *src = a.src_tables + (size_t)s * a.max_blocks;
+    const int32_t *dst = a.dst_tables + (size_t)s * a.max_blocks;
+    const int B = 1 << a.bshift, H = a.num_heads;
+
+    // Rows (of head kh, or of head 0 of all) that row j of the list moves between.
+    auto plan = [&](int buf, int j0) {
+        for (int k = tid; k < a.chunk; k += kMoveThreads) {
+            long long f = -1, t = -1;
+            const int j = j0 + k;
+            if (j < len) {
+                const int at = keep[j], prev = j > 0 ? keep[j - 1] : -1;
+                const long long sp = (long long)first + at, dp = (long long)first + j;
+                if (at <= prev || at < 0 || sp >= ctx) {
+                    report(a.status, PA_ERR_INVALID_ARG);
+                } else if ((sp >> a.bshift) >= a.max_blocks) {
+                    report(a.status, PA_ERR_BAD_BLOCK);
+                } else {
+                    const int sb = src[sp >> a.bshift], db = dst[dp >> a.bshift];
+                    if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) {
+                        report(a.status, PA_ERR_BAD_BLOCK);
+                    } else if (sb != db || sp != dp) {
+                        f = (((long long)sb * H + kh * heads_each) << a.bshift) + (sp & (B - 1));
+                        t = (((long long)db * H + kh * heads_each) << a.bshift) + (dp & (B - 1));
+                    }
+                }
+            }
+            from[buf][k] = f;
+            to[buf][k] = t;
+        }
+    };
+    const int c = tid % a.cols, r = tid / a.cols;
+    const int col = cg * a.cols + c;                    // vector of the row, over the list's heads
+    const bool mine = col < heads_each * vec && r < a.rows;
+    // column col is vector col % vec of head col / vec
+    const long long col_off =
+        ((long long)(col >> a.row_shift) << (a.bshift + a.row_shift)) + (col & (vec - 1));
+    plan(0, 0);
+    __syncthreads();
+    int buf = 0;
+    for (int j0 = 0; j0 < len; j0 += a.chunk, buf ^= 1) {
+        uint4 x[kUnroll];
+        if (mine) {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int i = r + k * a.rows;
+                if (i < a.chunk && from[buf][i] >= 0) x[k] = cache[(from[buf][i] << a.row_shift) + col_off];
+            }
+        }
+        if (j0 + a.chunk < len) plan(buf ^ 1, j0 + a.chunk);
+        __syncthreads();
+        if (mine) {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int i = r + k * a.rows;
+                if (i < a.chunk && to[buf][i] >= 0) cache[(to[buf][i] << a.row_shift) + col_off] = x[k];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+bool mis(const void *ptr, int n) { return (reinterpret_cast<uintptr_t>(ptr) & (n - 1)) != 0; }
+
+}  // namespace
+
+int launch_evict_select(int32_t *keep, int32_t *keep_lens, float *weights_out, const float *weights_in,
+                        int32_t weight_len, const int32_t *ctx_lens, int32_t n_seqs, int32_t num_heads,
+                        int32_t budget, int32_t recent, int32_t *status, void *stream) {
+    const char *who = "pa_evict_select";
+    if (n_seqs < 0 || n_seqs > 65535 || num_heads < 1 || weight_len < 0)
+        return fail(PA_ERR_INVALID_ARG, "%s: n_seqs=%d (<= 65535), num_heads=%d, weight_len=%d", who, n_seqs,
+                    num_heads, weight_len);
+    if (budget < 1 || recent < 0 || recent > budget)
+        return fail(PA_ERR_INVALID_ARG, "%s: budget=%d (>= 1), recent=%d (0 to budget)", who, budget, recent);
+    if (n_seqs == 0) return PA_OK;
+    if (!keep || !keep_lens || !ctx_lens || (weight_len > 0 && (!weights_out || !weights_in)))
+        return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (mis(keep, 4) || mis(keep_lens, 4) || mis(weights_out, 4) || mis(weights_in, 4) || mis(ctx_lens, 4) ||
+        mis(status, 4))
+        return fail(PA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+    SelectParams a{keep, keep_lens, weights_out, weights_in, ctx_lens, weight_len, budget, recent, num_heads, status};
+    const dim3 grid((unsigned)num_heads, (unsigned)n_seqs);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (weight_len <= kCached) {
+        const int bytes = weight_len * 4;
+        if (bytes > 32 * 1024)
+            e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kCached * 4);
+        if (e == cudaSuccess) evict_select_kernel<true><<<grid, kSelThreads, bytes, st>>>(a);
+    } else {
+        evict_select_kernel<false><<<grid, kSelThreads, 0, st>>>(a);
+    }
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+    return PA_OK;
+}
+
+int launch_compact_kv(void *const *k_caches, void *const *v_caches, int32_t num_layers,
+                      const int32_t *src_tables, const int32_t *dst_tables, const int32_t *src_lens,
+                      const int32_t *first, const int32_t *keep, const int32_t *keep_lens, int32_t keep_heads,
+                      int32_t keep_stride, int32_t n_seqs, int32_t max_blocks, const pa_pool_desc *d,
+                      int32_t *status, void *stream) {
+    const char *who = "pa_compact_kv";
+    std::string why;
+    if (!d) return fail(PA_ERR_INVALID_ARG, "%s: NULL desc", who);
+    if (!device_geometry_ok(d, &why)) return fail(PA_ERR_INVALID_ARG, "%s: %s", who, why.c_str());
+    if (num_layers < 0 || num_layers > kMaxMoveLayers || n_seqs < 0 || n_seqs > 65535 || max_blocks < 0 ||
+        keep_stride < 0)
+        return fail(PA_ERR_INVALID_ARG,
+                    "%s: num_layers=%d (<= %d), n_seqs=%d (<= 65535), max_blocks=%d, keep_stride=%d", who,
+                    num_layers, kMaxMoveLayers, n_seqs, max_blocks, keep_stride);
+    if (keep_heads != 1 && keep_heads != d->num_heads)
+        return fail(PA_ERR_INVALID_ARG, "%s: keep_heads=%d is neither 1 nor num_heads=%d", who, keep_heads,
+                    d->num_heads);
+    if (num_layers == 0 || n_seqs == 0 || keep_stride == 0) return PA_OK;
+    if (!k_caches || !v_caches || !src_tables || !dst_tables || !src_lens || !keep || !keep_lens)
+        return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    if (mis(src_tables, 4) || mis(dst_tables, 4) || mis(src_lens, 4) || mis(first, 4) || mis(keep, 4) ||
+        mis(keep_lens, 4) || mis(status, 4))
+        return fail(PA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+    CompactParams a{};
+    for (int l = 0; l < num_layers; ++l) {
+        if (!k_caches[l] || !v_caches[l] || mis(k_caches[l], 16) || mis(v_caches[l], 16))
+            return fail(PA_ERR_INVALID_ARG, "%s: cache pointer of layer %d NULL or not 16-byte aligned", who, l);
+        a.cache[2 * l] = static_cast<uint4 *>(k_caches[l]);
+        a.cache[2 * l + 1] = static_cast<uint4 *>(v_caches[l]);
+    }
+    a.src_tables = src_tables;
+    a.dst_tables = dst_tables;
+    a.src_lens = src_lens;
+    a.first = first;
+    a.keep = keep;
+    a.keep_lens = keep_lens;
+    a.num_heads = d->num_heads;
+    a.keep_heads = keep_heads;
+    a.keep_stride = keep_stride;
+    a.max_blocks = max_blocks;
+    a.num_blocks = d->num_blocks;
+    while ((1 << a.bshift) < d->block_size) ++a.bshift;
+    while ((8 << a.row_shift) < d->head_dim) ++a.row_shift;
+    a.status = status;
+    const int64_t columns = (int64_t)(d->num_heads / keep_heads) << a.row_shift;
+    a.cols = (int)std::min<int64_t>(columns, kMoveThreads);
+    a.rows = kMoveThreads / a.cols;
+    a.chunk = std::min(kMaxChunk, a.rows * kUnroll);
+    const int64_t gx = (columns + a.cols - 1) / a.cols * keep_heads;
+    if (gx > INT32_MAX) return fail(PA_ERR_INVALID_ARG, "%s: num_heads * head_dim too large", who);
+    compact_kv_kernel<<<dim3((unsigned)gx, (unsigned)n_seqs, (unsigned)(2 * num_layers)), kMoveThreads, 0,
+                        static_cast<cudaStream_t>(stream)>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+    return PA_OK;
+}
+
+}  // namespace pagedkv

@@ -417,6 +417,114 @@ int pa_seq_free_batch(pa_pool *pool, int32_t n, const int32_t *seq_ids) {
     return PA_OK;
 }
 
+// The sequences of a shortening call, each listed once and no shorter than
+// its new length; into pool->plan_seqs.
+static int plan_shorten(pa_pool *pool, const char *who, int32_t n_seqs, const int32_t *seq_ids,
+                        const int32_t *new_lens) {
+    if (!pool || n_seqs < 0 || (n_seqs > 0 && (!seq_ids || !new_lens)))
+        return fail(PA_ERR_INVALID_ARG, "%s: bad arguments", who);
+    const uint64_t epoch = ++pool->epoch;
+    try {
+        pool->plan_seqs.resize((size_t)n_seqs);
+    } catch (const std::bad_alloc &) {
+        return fail(PA_ERR_INVALID_ARG, "%s: out of host memory", who);
+    }
+    for (int32_t i = 0; i < n_seqs; ++i) {
+        auto it = pool->seqs.find(seq_ids[i]);
+        if (it == pool->seqs.end()) return fail(PA_ERR_NO_SEQ, "%s: no sequence %d", who, seq_ids[i]);
+        Seq &s = it->second;
+        if (s.stamp == epoch)
+            return fail(PA_ERR_INVALID_ARG, "%s: sequence %d listed twice", who, seq_ids[i]);
+        if (new_lens[i] < 0 || new_lens[i] > s.num_tokens)
+            return fail(PA_ERR_INVALID_ARG, "%s: sequence %d has %d tokens, not %d or more", who,
+                        seq_ids[i], s.num_tokens, new_lens[i]);
+        s.stamp = epoch;
+        pool->plan_seqs[(size_t)i] = &s;
+    }
+    return PA_OK;
+}
+
+// Drop the blocks past the first n_tokens tokens, last one first.  A last
+// block left partly filled leaves the prefix cache: later appends will write
+// into it.
+static void shorten(pa_pool *pool, Seq &s, int32_t n_tokens) {
+    const int32_t B = pool->block_size;
+    const size_t keep = (size_t)(((int64_t)n_tokens + B - 1) / B);
+    if (s.table.size() > keep) s.tver = next_table_version();
+    while (s.table.size() > keep) {
+        pool->release(s.table.back());
+        s.table.pop_back();
+    }
+    s.num_tokens = n_tokens;
+    if (n_tokens % B != 0) pool->uncache(s.table.back());
+}
+
+int pa_seq_truncate(pa_pool *pool, int32_t n_seqs, const int32_t *seq_ids, const int32_t *new_lens) {
+    const int rc = plan_shorten(pool, "pa_seq_truncate", n_seqs, seq_ids, new_lens);
+    if (rc != PA_OK) return rc;
+    for (int32_t i = 0; i < n_seqs; ++i) shorten(pool, *pool->plan_seqs[(size_t)i], new_lens[i]);
+    return PA_OK;
+}
+
+int pa_seq_compact(pa_pool *pool, int32_t n_seqs, const int32_t *seq_ids, const int32_t *new_lens,
+                   int32_t max_blocks, int32_t *src_tables_out, int32_t *src_lens_out,
+                   int32_t *dst_tables_out) {
+    const char *who = "pa_seq_compact";
+    const int rc = plan_shorten(pool, who, n_seqs, seq_ids, new_lens);
+    if (rc != PA_OK) return rc;
+    if (max_blocks < 0 || (n_seqs > 0 && (!src_lens_out || (max_blocks > 0 && (!src_tables_out || !dst_tables_out)))))
+        return fail(PA_ERR_INVALID_ARG, "%s: bad arguments", who);
+    // Blocks to replace: shared ones among those that will be rewritten, by
+    // the counts before the call (two sequences of the call that share a
+    // block both get another one, since each still reads it).
+    const int32_t B = pool->block_size;
+    std::vector<std::pair<int32_t, int32_t>> replace;   // (sequence of the call, table entry)
+    try {
+        for (int32_t i = 0; i < n_seqs; ++i) {
+            const Seq &s = *pool->plan_seqs[(size_t)i];
+            if ((int64_t)s.table.size() > max_blocks)
+                return fail(PA_ERR_INVALID_ARG, "%s: sequence %d has %zu blocks > max_blocks %d", who,
+                            seq_ids[i], s.table.size(), max_blocks);
+            if (new_lens[i] == s.num_tokens) continue;   // nothing moves
+            const int32_t nb = (int32_t)(((int64_t)new_lens[i] + B - 1) / B);
+            for (int32_t j = 0; j < nb; ++j)
+                if (pool->ref[(size_t)s.table[(size_t)j]] > 1) replace.emplace_back(i, j);
+        }
+    } catch (const std::bad_alloc &) {
+        return fail(PA_ERR_INVALID_ARG, "%s: out of host memory", who);
+    }
+    if ((int64_t)replace.size() > pool->count)
+        return fail(PA_ERR_OUT_OF_BLOCKS, "%s: need %zu blocks for shared ones, %lld free", who, replace.size(),
+                    (long long)pool->count);
+    auto put_row = [&](int32_t *out, int32_t i) {
+        const std::vector<int32_t> &t = pool->plan_seqs[(size_t)i]->table;
+        int32_t *row = out + (int64_t)i * max_blocks;
+        std::copy(t.begin(), t.end(), row);
+        std::fill(row + t.size(), row + max_blocks, -1);
+    };
+    for (int32_t i = 0; i < n_seqs; ++i) {
+        src_lens_out[i] = pool->plan_seqs[(size_t)i]->num_tokens;
+        if (max_blocks > 0) put_row(src_tables_out, i);
+    }
+    // all new blocks first, so that none is one that the call lets go
+    for (const auto &e : replace) {
+        Seq &s = *pool->plan_seqs[(size_t)e.first];
+        const int32_t shared = s.table[(size_t)e.second];
+        s.table[(size_t)e.second] = pool->pop_free();
+        s.tver = next_table_version();
+        pool->release(shared);
+    }
+    for (int32_t i = 0; i < n_seqs; ++i) {
+        Seq &s = *pool->plan_seqs[(size_t)i];
+        if (new_lens[i] != s.num_tokens) {
+            shorten(pool, s, new_lens[i]);
+            for (int32_t b : s.table) pool->uncache(b);   // rewritten
+        }
+        if (max_blocks > 0) put_row(dst_tables_out, i);
+    }
+    return PA_OK;
+}
+
 int pa_beam_prune(pa_pool *pool, int32_t n_groups, int32_t width, int32_t *beams,
                   const int32_t *counts, int32_t *next_id) {
     const char *who = "pa_beam_prune";
