@@ -50,8 +50,57 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "tc_device.cuh"
 
 namespace pagedkv {
+
+namespace tc {
+// 16 or 64 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void ld64(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,"
+        "%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,"
+        "%62,%63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]),
+          "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+          "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
+          "=r"(r[63])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void st64(uint32_t taddr, const uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,"
+        "%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,"
+        "%61,%62,%63,%64};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+          "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+          "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+          "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(r[32]), "r"(r[33]), "r"(r[34]), "r"(r[35]),
+          "r"(r[36]), "r"(r[37]), "r"(r[38]), "r"(r[39]), "r"(r[40]), "r"(r[41]), "r"(r[42]),
+          "r"(r[43]), "r"(r[44]), "r"(r[45]), "r"(r[46]), "r"(r[47]), "r"(r[48]), "r"(r[49]),
+          "r"(r[50]), "r"(r[51]), "r"(r[52]), "r"(r[53]), "r"(r[54]), "r"(r[55]), "r"(r[56]),
+          "r"(r[57]), "r"(r[58]), "r"(r[59]), "r"(r[60]), "r"(r[61]), "r"(r[62]), "r"(r[63])
+        : "memory");
+}
+}  // namespace tc
 
 namespace {
 
@@ -59,7 +108,8 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHeaderBytes = 256;    // workspace head: unit ticket, number of cut sequences
 constexpr int kUnitSlots = 3;        // units a CTA has open
-constexpr int kMinPartTokens = 64;
+constexpr int kTile = 128;           // tokens of a tile: the lanes of tensor memory
+constexpr float kRescaleLog2 = 8.f;  // tensor-memory kernel: how far a row's maximum may pass its reference
 
 struct TreeParams {
     __half *out;
@@ -78,13 +128,13 @@ struct TreeParams {
     float *scores;             // [S][H][score_stride] scores in log2 units
     int32_t *status;
     int32_t n_seqs, num_heads, num_blocks, max_blocks, bshift, max_q, q_rows, cap;
-    int32_t stages, stage_tokens;
+    int32_t stages;
     int32_t score_stride, weight_len;
     float qscale;              // scale * log2(e)
 };
 
 struct TreeMaps {
-    CUtensorMap k, v;
+    CUtensorMap k, v, q;
 };
 
 // ---------------------------------------------------------------- helpers
@@ -93,27 +143,6 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// d += a b: 16 x 16 fp16 (row) times 16 x 8 fp16 (column), fp32 accumulators.
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -127,6 +156,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
         "[%0], [%1, {%2, %2, %2, %3}], [%4], %5;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c3), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -170,63 +208,19 @@ __device__ __forceinline__ int warp_incl_scan(int v, int lane) {
     return v;
 }
 
-// ------------------------------------------------------------ main kernel
-
-template <int D, int GH, int MW>
-struct TreeCfg {
-    static constexpr int NP = D / 64;                       // 64-column panels of a row
-    static constexpr int NR = 16 * MW;                      // query rows, padded
-    static constexpr int WARPS = GH * MW;                   // consumer warps
-    static constexpr int THREADS = (WARPS + 1) * 32;
-    static constexpr int PER_SM = WARPS >= 8 ? 1 : WARPS >= 4 ? 2 : WARPS >= 2 ? 3 : 4;
-    static constexpr int MAX_STAGES = 16;
-    // fixed shared memory before the ring (1024-byte aligned)
-    static constexpr int SDESC = 0;                                   // int4 per stage
-    static constexpr int BARS = SDESC + MAX_STAGES * 16;              // full, empty, unit empty
-    static constexpr int VARS = BARS + (2 * MAX_STAGES + kUnitSlots) * 8 + 8;
-    static constexpr int UNITS = (VARS + 16 + 15) / 16 * 16;          // 64 B per slot
-    static constexpr int MASKS = UNITS + kUnitSlots * 64;             // 64 x u64 per slot
-    static constexpr int PLAN = MASKS + kUnitSlots * 64 * 8;          // pre[S+1], len[S], order[S]
-    static int plan_bytes(int S) { return (S + 1) * 4 + S * 4 + (S + 1) / 2 * 4; }
-    static int bytes(int S, int ring) { return PLAN + plan_bytes(S) + 1024 + ring; }
-};
-
-enum { FLAG_FIRST = 1, FLAG_LAST = 2, FLAG_END = 4 };
-
-template <int D, int GH, int MW, bool SCORES>
-__global__ void __launch_bounds__((GH * MW + 1) * 32, (TreeCfg<D, GH, MW>::PER_SM))
-    tree_attention_kernel(const TreeParams p, const __grid_constant__ TreeMaps maps) {
-    using Cfg = TreeCfg<D, GH, MW>;
-    constexpr int NP = Cfg::NP, NR = Cfg::NR;
-    const uint32_t HALF = (uint32_t)GH * p.stage_tokens * D * 2, STAGE = 2 * HALF;   // keys, then values
-    extern __shared__ __align__(16) uint8_t smem[];
-    int4 *sdesc = reinterpret_cast<int4 *>(smem + Cfg::SDESC);
-    const uint32_t bar_full = smem_addr(smem + Cfg::BARS);
-    const uint32_t bar_empty = bar_full + Cfg::MAX_STAGES * 8;
-    const uint32_t bar_unit = bar_empty + Cfg::MAX_STAGES * 8;
-    int32_t *vars = reinterpret_cast<int32_t *>(smem + Cfg::VARS);   // ordered, cut sequences
-    int32_t *units = reinterpret_cast<int32_t *>(smem + Cfg::UNITS);
-    uint64_t *masks = reinterpret_cast<uint64_t *>(smem + Cfg::MASKS);
-    const int S = p.n_seqs, H = p.num_heads, HG = H / GH;
-    int32_t *pre = reinterpret_cast<int32_t *>(smem + Cfg::PLAN);    // parts before the i-th in order
-    int32_t *len = pre + S + 1;                                      // blocks of sequence s
-    uint16_t *order = reinterpret_cast<uint16_t *>(len + S);
-    const uint32_t ring = (smem_addr(order + S) + 1023u) & ~1023u;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int stages = p.stages, bshift = p.bshift, B = 1 << bshift;
-
-    // ---- the plan
-    if (tid == 0) {
-        for (int i = 0; i < stages; ++i) {
-            mbar_init(bar_full + 8 * i, 1);
-            mbar_init(bar_empty + 8 * i, Cfg::WARPS);
-        }
-        for (int i = 0; i < kUnitSlots; ++i) mbar_init(bar_unit + 8 * i, Cfg::WARPS);
-        fence_barrier_init();
-    }
-    for (int s = tid; s < S; s += Cfg::THREADS) {
+// The launch's work plan, the same in every CTA, by all its threads: len[s]
+// tiles of sequence s (0: no work), order[] the sequences with work, pre[i]
+// the parts of those before the i-th; vars: how many have work, how many of
+// them are cut.  A part is read once for each of HG head groups.  CTA 0 also
+// leaves the cut sequences (weights form: every sequence's parts) for the kernels
+// that join them.
+template <bool SCORES>
+__device__ void make_plan(const TreeParams &p, int32_t *pre, int32_t *len, uint16_t *order, int32_t *vars,
+                          int32_t *counts, int HG) {
+    const int S = p.n_seqs, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int s = tid; s < S; s += (int)blockDim.x) {
         const SeqRows r = rows_of<SCORES>(p, s, blockIdx.x == 0);
-        len[s] = r.n > 0 ? (r.ctx + B - 1) >> bshift : 0;
+        len[s] = r.n > 0 ? (r.ctx + kTile - 1) / kTile : 0;
     }
     __syncthreads();
     if (warp == 0) {
@@ -244,60 +238,65 @@ __global__ void __launch_bounds__((GH * MW + 1) * 32, (TreeCfg<D, GH, MW>::PER_S
             some += __shfl_xor_sync(kAll, some, off);
             longest = max(longest, __shfl_xor_sync(kAll, longest, off));
         }
-        const int slots = gridDim.x;
-        const int share = (int)((total * HG + slots - 1) / slots);   // blocks a slot has to read
-        int P = max(1, kMinPartTokens >> bshift);
-        if ((long long)some * HG < slots) {
-            // few sequences: the smallest part size whose units fit the slots
-            // at once; every lane tries one size of a grid
-            int lo = max(P, share), hi = max(lo, longest);
-            while (lo < hi) {
-                const int step = (hi - lo + 30) / 31, cand = min(hi, lo + lane * step);
-                long long units_n = 0;
-                for (int s = 0; s < S; ++s) units_n += (len[s] + cand - 1) / cand;
-                const unsigned fits = __ballot_sync(kAll, units_n * HG <= slots || cand == hi);
-                const int f = __ffs(fits) - 1;   // (lane 31 reaches hi)
-                const int nhi = min(hi, lo + f * step);
-                lo = f == 0 ? nhi : min(hi, lo + (f - 1) * step + 1);
-                hi = nhi;
+        // How many tiles a part may have, P.  A unit costs its tiles, about one
+        // more to get going, and where it is a part of a cut sequence the
+        // writing and joining of its rows.
+        const int slots = gridDim.x, extra = kTile + 2 * p.max_q;     // in tokens
+        int P = longest, cut_parts;
+        if ((long long)some * HG < 4 * slots) {
+            // few units: the longest sequence in 1 to 32 parts, a lane each,
+            // by what the last SM would be done at
+            const int mine = (longest + lane) / (lane + 1);
+            long long units_n = 0;
+            int cuts = 0;
+            for (int s = 0; s < S; ++s) {
+                const int parts = mine ? (len[s] + mine - 1) / mine : 0;
+                units_n += parts;
+                cuts += parts > 1 ? parts : 0;
             }
-            P = hi;
+            units_n *= HG;
+            const float all = ((float)total * HG * kTile + (float)(units_n * (lane ? extra : kTile))) / slots;
+            float end = fmaxf(units_n > slots ? all + 0.5f * mine * kTile : 0.f, (float)mine * kTile + extra);
+            end = fmaxf(end, all);
+            if (cuts > p.cap) end = INFINITY;
+            float best = end;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) best = fminf(best, __shfl_xor_sync(kAll, best, off));
+            P = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, end == best)) - 1);
         } else {
-            P = max(P, (share + 1) / 2);
+            // many: parts of a quarter of an SM's share
+            P = (int)((total * HG + 4 * slots - 1) / (4 * slots));
         }
-        int ncls[5], cut_parts;
-        while (true) {   // (the cap is never passed: parts of at least half a share each)
+        P = max(P, 1);
+        while (true) {   // (more than the cap only where the first case found none)
             cut_parts = 0;
-#pragma unroll
-            for (int k = 0; k < 5; ++k) ncls[k] = 0;
-            for (int s = lo_s; s < hi_s; ++s) {
-                const int l = len[s];
-                if (l > P) cut_parts += (l + P - 1) / P;
-                const int cls = l > P ? 0 : 4 * (long long)l > 3ll * P ? 1 : 2ll * l > P ? 2 : 4ll * l > P ? 3 : 4;
-#pragma unroll
-                for (int k = 0; k < 5; ++k) ncls[k] += l > 0 && cls == k;
-            }
+            for (int s = lo_s; s < hi_s; ++s)
+                if (len[s] > P) cut_parts += (len[s] + P - 1) / P;
             if (__reduce_add_sync(kAll, cut_parts) <= p.cap) break;
             P *= 2;
         }
-        int base[5], start = 0, n_cut = 0;
-#pragma unroll
-        for (int k = 0; k < 5; ++k) {
-            const int incl = warp_incl_scan(ncls[k], lane);
-            base[k] = start + incl - ncls[k];
-            start += __shfl_sync(kAll, incl, 31);
-            if (k == 0) n_cut = start;
+        // counting sort by size class: 0 the cut ones, 1 .. 31 the others, long
+        // ones first; counts[lane][class], a row of 33
+        const int top = min(P, longest);
+        auto cls = [&](int l) { return l > P ? 0 : 1 + (int)((long long)(top - l) * 30 / top); };
+        for (int k = 0; k < 32; ++k) counts[lane * 33 + k] = 0;
+        __syncwarp();
+        for (int s = lo_s; s < hi_s; ++s)
+            if (len[s] > 0) ++counts[lane * 33 + cls(len[s])];
+        __syncwarp();
+        int mine_cls = 0;                // lane = class: where its lanes' sequences start
+        for (int k = 0; k < 32; ++k) mine_cls += counts[k * 33 + lane];
+        const int incl_cls = warp_incl_scan(mine_cls, lane);
+        int at = incl_cls - mine_cls;
+        for (int k = 0; k < 32; ++k) {
+            const int c = counts[k * 33 + lane];
+            counts[k * 33 + lane] = at;
+            at += c;
         }
-        for (int s = lo_s; s < hi_s; ++s) {
-            const int l = len[s];
-            if (l == 0) continue;
-            const int cls = l > P ? 0 : 4 * (long long)l > 3ll * P ? 1 : 2ll * l > P ? 2 : 4ll * l > P ? 3 : 4;
-            int r = 0;
-#pragma unroll
-            for (int k = 0; k < 5; ++k)
-                if (cls == k) r = base[k]++;
-            order[r] = (uint16_t)s;
-        }
+        __syncwarp();
+        const int start = __shfl_sync(kAll, incl_cls, 31), n_cut = __shfl_sync(kAll, incl_cls, 0);
+        for (int s = lo_s; s < hi_s; ++s)
+            if (len[s] > 0) order[counts[lane * 33 + cls(len[s])]++] = (uint16_t)s;
         __syncwarp();
         const int n_ord = start, per2 = (n_ord + 31) / 32;
         const int lo_i = min(n_ord, lane * per2), hi_i = min(n_ord, lo_i + per2);
@@ -315,49 +314,228 @@ __global__ void __launch_bounds__((GH * MW + 1) * 32, (TreeCfg<D, GH, MW>::PER_S
         }
     }
     __syncthreads();
-    const int n_ord = vars[0], n_units = pre[n_ord] * HG;
     if (blockIdx.x == 0) {   // for the kernels that join the parts
         const int n_cut = vars[1];
         if (tid == 0) p.header[1] = n_cut;
-        for (int i = tid; i < n_cut; i += Cfg::THREADS) {
+        for (int i = tid; i < n_cut; i += (int)blockDim.x) {
             const int s = order[i];
             const SeqRows r = rows_of<SCORES>(p, s, false);
             p.cut[i] = make_int4(s, pre[i], pre[i + 1] - pre[i], r.n);
         }
         if (SCORES) {
-            for (int s = tid; s < S; s += Cfg::THREADS)
+            for (int s = tid; s < S; s += (int)blockDim.x)
                 if (len[s] == 0) p.plan[s] = make_int2(0, 0);
-            for (int i = tid; i < n_ord; i += Cfg::THREADS)
+            for (int i = tid; i < vars[0]; i += (int)blockDim.x)
                 p.plan[order[i]] = make_int2(pre[i], pre[i + 1] - pre[i]);
         }
     }
 
-    if (warp == Cfg::WARPS) {
+}
+
+// Which nodes see each node of a sequence (itself and its descendants): every
+// node's ancestors by doubling the parent links (lane l takes nodes l and
+// l + 32), then the 64 x 64 bits transposed.
+template <bool SCORES>
+__device__ __forceinline__ void nodes_seen_by(const TreeParams &p, const SeqRows &r, int lane, uint64_t *out) {
+    uint64_t m[2];
+    int up[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = lane + 32 * e;
+        up[e] = i - 1;
+        if (!SCORES && p.parents && i < r.n) {
+            up[e] = p.parents[r.row0 + i];
+            if (up[e] < -1 || up[e] >= i) {
+                report(p.status, PA_ERR_INVALID_ARG);
+                up[e] = -1;
+            }
+        }
+        m[e] = 1ull << i;
+    }
+    if (SCORES || !p.parents) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) m[e] |= (1ull << (lane + 32 * e)) - 1;
+    } else {
+        for (int k = 1; k < r.n; k <<= 1) {
+            uint64_t add[2];
+            int far[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = up[e] & 31;
+                const bool second = up[e] >= 32;
+                const uint64_t a = __shfl_sync(kAll, m[0], t), b = __shfl_sync(kAll, m[1], t);
+                const int fa = __shfl_sync(kAll, up[0], t), fb = __shfl_sync(kAll, up[1], t);
+                add[e] = up[e] < 0 ? 0 : (second ? b : a);
+                far[e] = up[e] < 0 ? -1 : (second ? fb : fa);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[e] |= add[e];
+                up[e] = far[e];
+            }
+        }
+    }
+    for (int j = 0; j < r.n; ++j) {
+        const uint32_t lo = __ballot_sync(kAll, lane < r.n && ((m[0] >> j) & 1));
+        const uint32_t hi = __ballot_sync(kAll, lane + 32 < r.n && ((m[1] >> j) & 1));
+        if (lane == 0) out[j] = (uint64_t)hi << 32 | lo;
+    }
+}
+
+// ------------------------------------------------------------ main kernel
+
+constexpr int kSoftmaxWarps = 4, kProducer = 4, kProducts = 5, kQueries = 6, kThreads = 224;
+constexpr int kMinStages = 4, kMaxStages = 12;
+
+template <int D, int NQ>
+struct TreeCfg {
+    static constexpr int NP = D / 64;                        // 64-column panels of a row
+    static constexpr int HALF = kTile * D * 2;               // keys or values of a tile: a ring stage
+    // tensor-memory columns: two S, O (a power of two in all)
+    static constexpr uint32_t S_COL = 0, O_COL = 2 * NQ, COLS = 4 * NQ;
+    static constexpr int BARS = 0;                           // full, empty; units; q, s, p, o, done
+    static constexpr int VARS = BARS + (2 * kMaxStages + 2 * kUnitSlots + 2 + 2 + 2 + 1 + 1) * 8;
+    static constexpr int UNITS = (VARS + 16 + 15) / 16 * 16;
+    static constexpr int SEEN = UNITS + kUnitSlots * 64;     // 64 x u64 per slot
+    static constexpr int RED = SEEN + kUnitSlots * 64 * 8;   // per warp and row
+    static constexpr int REF = RED + kSoftmaxWarps * NQ * 4; // reference maxima, corrections
+    static constexpr int PLAN = REF + 2 * NQ * 4;            // pre[S+1], len[S], order[S]
+    static constexpr int Q_BYTES = NQ * D * 2;               // [panel][row][128 bytes]
+    static constexpr int P_BYTES = kTile * 128;              // [token][128 bytes], rows of 64 columns
+    static int plan_bytes(int S) { return (S + 1) * 4 + S * 4 + (S + 1) / 2 * 4; }
+    static int bytes(int S, int stages) {
+        return PLAN + plan_bytes(S) + 1024 + Q_BYTES + 2 * P_BYTES + stages * HALF;
+    }
+};
+
+// Eight fp32 from shared memory, 16-byte aligned.
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// One barrier of the softmax warps.
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxWarps * 32) : "memory");
+}
+// The same; whether v held in any (all) of their threads.
+__device__ __forceinline__ bool softmax_any(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "n"(kSoftmaxWarps * 32)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool softmax_all(bool v) { return !softmax_any(!v); }
+
+// Combines N values over a warp's lanes: on return v[0 .. max(N / 32, 1)) are
+// the results for values first, first + 1, ... (every lane has a share).
+template <int N, typename Op>
+__device__ __forceinline__ int warp_combine(float (&v)[N], int lane, Op op) {
+    int first = 0;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+        const int off = 16 >> k, half = N >> (k + 1);
+        if (half >= 1) {
+            const bool upper = (lane & off) != 0;
+#pragma unroll
+            for (int i = 0; i < half; ++i) {
+                const float send = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
+                v[i] = op(keep, __shfl_xor_sync(kAll, send, off));
+            }
+            if (upper) first += half;
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(kAll, v[0], off));
+        }
+    }
+    return first;
+}
+
+template <int D, int NQ, bool SCORES>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attention_kernel(const TreeParams p, const __grid_constant__ TreeMaps maps) {
+    using Cfg = TreeCfg<D, NQ>;
+    constexpr int NP = Cfg::NP, HALF = Cfg::HALF;
+    constexpr int G = SCORES ? 1 : NQ / 8;               // groups of 8 rows worked on
+    constexpr int R = SCORES ? 1 : NQ;                   // rows worked on
+    extern __shared__ __align__(16) uint8_t smem[];
+    const uint32_t bar_full = smem_addr(smem + Cfg::BARS), bar_empty = bar_full + kMaxStages * 8;
+    const uint32_t bar_unit = bar_empty + kMaxStages * 8, bar_unit_free = bar_unit + kUnitSlots * 8;
+    const uint32_t bar_q = bar_unit_free + kUnitSlots * 8, bar_q_free = bar_q + 8, bar_s = bar_q_free + 8,
+                   bar_p = bar_s + 16, bar_o = bar_p + 16, bar_done = bar_o + 8;
+    int32_t *vars = reinterpret_cast<int32_t *>(smem + Cfg::VARS);    // [2]: tensor-memory address
+    int32_t *units = reinterpret_cast<int32_t *>(smem + Cfg::UNITS);
+    uint64_t *seen = reinterpret_cast<uint64_t *>(smem + Cfg::SEEN);
+    float *red = reinterpret_cast<float *>(smem + Cfg::RED);
+    float *ref = reinterpret_cast<float *>(smem + Cfg::REF), *corr = ref + NQ;
+    const int S = p.n_seqs, H = p.num_heads;
+    int32_t *pre = reinterpret_cast<int32_t *>(smem + Cfg::PLAN);
+    int32_t *len = pre + S + 1;
+    uint16_t *order = reinterpret_cast<uint16_t *>(len + S);
+    uint8_t *tiles_at = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(order + S) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int stages = p.stages, bshift = p.bshift, B = 1 << bshift, bps = kTile >> bshift;
+    // (for D = 64 the second half of V^T's rows is whatever lies 1 KB on: the
+    // ring is followed by P)
+    const uint32_t ring = smem_addr(tiles_at), sP = ring + stages * HALF, sQ = sP + 2 * Cfg::P_BYTES;
+
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < kUnitSlots; ++i) {
+            mbar_init(bar_unit + 8 * i, 1);
+            mbar_init(bar_unit_free + 8 * i, kSoftmaxWarps + 2);
+        }
+        mbar_init(bar_q, 1);
+        mbar_init(bar_q_free, 1);
+        mbar_init(bar_s, 1);
+        mbar_init(bar_s + 8, 1);
+        mbar_init(bar_p, kSoftmaxWarps);
+        mbar_init(bar_p + 8, kSoftmaxWarps);
+        mbar_init(bar_o, 1);
+        mbar_init(bar_done, 1);
+        fence_barrier_init();
+    }
+    if (warp == kProducts) tc::alloc(smem_addr(&vars[2]), Cfg::COLS);
+    make_plan<SCORES>(p, pre, len, order, vars, reinterpret_cast<int32_t *>(tiles_at), H);
+    // columns of P that no row writes have to hold finite numbers
+    for (int i = tid; i < 2 * Cfg::P_BYTES / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(tiles_at + stages * HALF)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = (uint32_t)vars[2];
+    const int n_ord = vars[0], n_units = pre[n_ord] * H;
+    bool ok = true;
+
+    if (warp == kProducer) {
         // ================================================ producer warp
         const uint64_t policy = l2_evict_first_policy();
-        const int bps = p.stage_tokens >> bshift;                    // blocks a stage
-        const uint32_t blk_bytes = (uint32_t)GH * D * 2u << bshift;
-        const int groups_per_run = GH << bshift >> 3;    // 8-row groups of a box
-        const int groups_per_block = (H << bshift) >> 3;
-        bool ok = true;
-        int st = 0;
-        uint32_t use = 0;        // times the ring has wrapped
-        int k_unit = 0, issued = 0;
-
+        const uint32_t blk_bytes = (uint32_t)D * 2u << bshift;
+        const int run = B >> 3;                          // 8-row groups of a block's head
+        int st = 0, k_unit = 0, issued = 0;
+        uint32_t use = 0;
         struct Pending {
-            int ticket, s, h0, gp, parts, b0, nb, tbl;
+            int ticket, s, h, gp, parts, b0, nb, tbl;
             SeqRows r;
         };
         // Names the unit of a ticket and starts the loads it needs.
         auto prepare = [&](int ticket) {
             Pending u;
             u.ticket = ticket;
-            u.s = u.h0 = u.gp = u.parts = u.b0 = u.nb = 0;
+            u.s = u.h = u.gp = u.parts = u.b0 = u.nb = 0;
             u.tbl = -1;
             u.r.n = u.r.row0 = u.r.ctx = 0;
             if (ticket >= n_units) return u;
-            u.gp = ticket / HG;
-            u.h0 = (ticket - u.gp * HG) * GH;
+            u.gp = ticket / H;
+            u.h = ticket - u.gp * H;
             int lo = 0, hi = n_ord - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
@@ -366,364 +544,397 @@ __global__ void __launch_bounds__((GH * MW + 1) * 32, (TreeCfg<D, GH, MW>::PER_S
             u.s = order[lo];
             u.parts = pre[lo + 1] - pre[lo];
             const int part = u.gp - pre[lo], l = len[u.s];
-            u.b0 = (int)((long long)part * l / u.parts);
-            u.nb = (int)((long long)(part + 1) * l / u.parts) - u.b0;
-            if (lane < u.nb) u.tbl = p.block_tables[(size_t)u.s * p.max_blocks + u.b0 + lane];
+            u.b0 = (int)((long long)part * l / u.parts) * bps;
+            u.nb = (int)((long long)(part + 1) * l / u.parts) * bps - u.b0;
+            // (the sequence's last blocks may be fewer)
+            if (u.b0 + lane < p.max_blocks && lane < u.nb)
+                u.tbl = p.block_tables[(size_t)u.s * p.max_blocks + u.b0 + lane];
             u.r = rows_of<SCORES>(p, u.s, false);
             return u;
         };
-
+        // The next free stage of the ring.
+        auto stage = [&]() {
+            if (use > 0) ok = mbar_wait_bounded(bar_empty + 8 * st, (use - 1) & 1u, p.status, true);
+            ok = __all_sync(kAll, ok);
+            return ok;
+        };
         int t_next = 0;
         Pending cur = prepare(blockIdx.x);
         if (lane == 0) t_next = (int)gridDim.x + atomicAdd(p.header, 1);
-        while (ok && cur.ticket < n_units) {
-            const int tn = __shfl_sync(kAll, t_next, 0);
-            if (lane == 0 && tn < n_units) t_next = (int)gridDim.x + atomicAdd(p.header, 1);
-            const Pending nxt = prepare(tn);
+        while (true) {
+            const bool last = cur.ticket >= n_units;     // one more descriptor: the end
             const int slot = k_unit % kUnitSlots, slot_use = k_unit / kUnitSlots;
-            if (slot_use > 0 && !mbar_wait_bounded(bar_unit + 8 * slot, (uint32_t)(slot_use - 1) & 1u,
-                                                   p.status, true)) {
-                report(p.status, PA_ERR_TIMEOUT);
-                ok = false;
-            }
+            if (slot_use > 0)
+                ok = mbar_wait_bounded(bar_unit_free + 8 * slot, (uint32_t)(slot_use - 1) & 1u, p.status, true);
             ok = __all_sync(kAll, ok);
             if (!ok) break;
             int32_t *u = units + slot * 16;
             const int base = cur.r.ctx - cur.r.n;
+            cur.nb = min(cur.nb, ((cur.r.ctx + B - 1) >> bshift) - cur.b0);
             if (lane == 0) {
+                const int end = min(cur.r.ctx, (cur.b0 + cur.nb) << bshift);
                 u[0] = cur.s;
-                u[1] = cur.h0;
+                u[1] = cur.h;
                 u[2] = cur.gp;
                 u[3] = cur.parts;
-                u[4] = cur.r.ctx;
-                u[5] = base;
-                u[6] = cur.r.n;
-                u[7] = cur.r.row0;
+                u[4] = cur.b0 << bshift;                     // first token
+                u[5] = last ? 0 : end - u[4];                // tokens
+                u[6] = base;
+                u[7] = cur.r.n;
+                u[8] = cur.r.row0;
             }
-            if ((cur.b0 + cur.nb) << bshift > base) {
-                // which nodes each node sees: its ancestors and itself, by
-                // doubling the parent links
-                uint64_t m[2];
-                int up[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = lane + 32 * e;
-                    up[e] = i - 1;
-                    if (!SCORES && p.parents && i < cur.r.n) {
-                        up[e] = p.parents[cur.r.row0 + i];
-                        if (up[e] < -1 || up[e] >= i) {
-                            report(p.status, PA_ERR_INVALID_ARG);
-                            up[e] = -1;
-                        }
-                    }
-                    m[e] = 1ull << i;
-                }
-                if (SCORES || !p.parents) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) m[e] |= (1ull << (lane + 32 * e)) - 1;
-                } else {
-                    for (int k = 1; k < cur.r.n; k <<= 1) {
-                        uint64_t add[2];
-                        int far[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int t = up[e] & 31;
-                            const bool second = up[e] >= 32;
-                            const uint64_t a = __shfl_sync(kAll, m[0], t), b = __shfl_sync(kAll, m[1], t);
-                            const int fa = __shfl_sync(kAll, up[0], t), fb = __shfl_sync(kAll, up[1], t);
-                            add[e] = up[e] < 0 ? 0 : (second ? b : a);
-                            far[e] = up[e] < 0 ? -1 : (second ? fb : fa);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            m[e] |= add[e];
-                            up[e] = far[e];
-                        }
-                    }
-                }
-                masks[slot * 64 + lane] = m[0];
-                masks[slot * 64 + 32 + lane] = m[1];
-            }
+            if (!last && (cur.b0 + cur.nb) << bshift > base)
+                nodes_seen_by<SCORES>(p, cur.r, lane, seen + slot * 64);
             __syncwarp();
+            if (lane == 0) mbar_arrive(bar_unit + 8 * slot);
+            ++k_unit;
+            if (last) break;
+            const int tn = __shfl_sync(kAll, t_next, 0);
+            if (lane == 0 && tn < n_units) t_next = (int)gridDim.x + atomicAdd(p.header, 1);
+            const Pending nxt = prepare(tn);
             const int32_t *trow = p.block_tables + (size_t)cur.s * p.max_blocks + cur.b0;
             int tbl = cur.tbl;
             for (int b = 0; b < cur.nb; b += bps) {
                 if (b > 0 && (b & 31) == 0) tbl = b + lane < cur.nb ? trow[b + lane] : -1;
                 const int here = min(bps, cur.nb - b);
-                // one lane a block of the stage
+                // one lane a block of the tile
                 const int phys = __shfl_sync(kAll, tbl, (b & 31) + (lane < here ? lane : 0));
                 const bool good = lane < here && phys >= 0 && phys < p.num_blocks;
-                const unsigned goods = __ballot_sync(kAll, good);
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(kAll, good)) * blk_bytes;
                 if (lane < here && !good) report(p.status, PA_ERR_BAD_BLOCK);
-                const uint32_t full = bar_full + 8 * st;
-                if (use > 0 && !mbar_wait_bounded(bar_empty + 8 * st, (use - 1) & 1u, p.status, true)) {
-                    report(p.status, PA_ERR_TIMEOUT);
-                    ok = false;
+                const int grp = (phys * H + cur.h) * run;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {         // the keys' stage, the values' stage
+                    if (!stage()) break;
+                    const uint32_t full = bar_full + 8 * st;
+                    if (lane == 0) {
+                        if (bytes) mbar_arrive_expect_tx(full, bytes);
+                        else mbar_arrive(full);
+                    }
+                    __syncwarp();
+                    if (good)
+                        tma_load_4d(ring + st * HALF + lane * blk_bytes, kv ? &maps.v : &maps.k, grp, full, policy);
+                    ++issued;
+                    if (++st == stages) {
+                        st = 0;
+                        ++use;
+                    }
                 }
-                ok = __all_sync(kAll, ok);
                 if (!ok) break;
-                if (lane == 0) {
-                    const int tok0 = (cur.b0 + b) << bshift;
-                    const int nv = min(here << bshift, cur.r.ctx - tok0);
-                    const int flags = (b == 0 ? FLAG_FIRST : 0) | (b + bps >= cur.nb ? FLAG_LAST : 0);
-                    sdesc[st] = make_int4(slot, flags, tok0, nv);
-                    const uint32_t bytes = (uint32_t)__popc(goods) * 2u * blk_bytes;
-                    if (bytes) mbar_arrive_expect_tx(full, bytes);
-                    else mbar_arrive(full);
-                }
-                __syncwarp();
-                if (good) {
-                    const uint32_t dst = ring + st * STAGE + lane * blk_bytes;
-                    const int grp = phys * groups_per_block + (cur.h0 / GH) * groups_per_run;
-                    tma_load_4d(dst, &maps.k, grp, full, policy);
-                    tma_load_4d(dst + HALF, &maps.v, grp, full, policy);
-                }
-                ++issued;
-                if (++st == stages) {
-                    st = 0;
-                    ++use;
-                }
             }
-            ++k_unit;
+            if (!ok) break;
             cur = nxt;
         }
-        if (ok) {   // the end of the stream
-            if (use > 0 && !mbar_wait_bounded(bar_empty + 8 * st, (use - 1) & 1u, p.status, true)) {
-                report(p.status, PA_ERR_TIMEOUT);
-                ok = false;
-            }
-            ok = __all_sync(kAll, ok);
-            if (ok && lane == 0) {
-                sdesc[st] = make_int4(0, FLAG_END, 0, 0);
-                mbar_arrive(bar_full + 8 * st);
-            }
-        }
         if (!ok) {   // every issued copy lands before the CTA can exit
+            if (lane == 0) report(p.status, PA_ERR_TIMEOUT);
             for (int k = max(0, issued - stages); k < issued; ++k)
                 mbar_wait_bounded(bar_full + 8 * (k % stages), (uint32_t)(k / stages) & 1u, p.status, false);
         }
-        return;
-    }
-
-    // ==================================================== consumer warps
-    const int hw = warp / MW, mw = warp - hw * MW;       // head of the group, row tile
-    const int g = lane >> 2, c = lane & 3;
-    uint4 ql[NP][2], qh[NP][2];                          // rows g and g + 8: dims 64 pn + 16c + 8u ..
-    float o[NP][8][4];
-    float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
-    int u_s = 0, u_h = 0, u_gp = 0, u_parts = 0, u_base = 0, u_n = 0, u_row0 = 0;
-    const uint32_t koff0 = (uint32_t)g * 128u + (uint32_t)((2 * c) ^ g) * 16u;   // u = 0; u = 1: ^ 16
-    const uint32_t voff0 = (uint32_t)(2 * c) * 128u + (uint32_t)(g ^ (2 * c)) * 16u;
-    const uint32_t voff1 = (uint32_t)(2 * c + 1) * 128u + (uint32_t)(g ^ (2 * c + 1)) * 16u;
-    const uint32_t blk_bytes = (uint32_t)GH * D * 2u << bshift;
-    const int r0 = mw * 16 + g;                          // this lane's rows: r0, r0 + 8
-
-    int st = 0;
-    uint32_t use = 0;
-    while (true) {
-        if (!mbar_wait_bounded(bar_full + 8 * st, use & 1u, p.status, true)) {
-            report(p.status, PA_ERR_TIMEOUT);
-            return;
-        }
-        const int4 d = sdesc[st];
-        if (d.y & FLAG_END) return;
-        if (d.y & FLAG_FIRST) {
-            const int32_t *u = units + d.x * 16;
-            u_s = u[0];
-            u_h = u[1] + hw;
-            u_gp = u[2];
-            u_parts = u[3];
-            u_base = u[5];
-            u_n = u[6];
-            u_row0 = u[7];
-            m0 = m1 = -INFINITY;
-            l0 = l1 = 0.f;
+    } else if (warp == kQueries) {
+        // ================================================ queries, one thread
+        // (a warp of its own: the next unit's keys and values are on their way
+        // before this unit's last product has let go of Q)
+        if (lane == 0) {
+            uint32_t k = 0;
+            for (;; ++k) {
+                const int slot = k % kUnitSlots;
+                ok = mbar_wait_bounded(bar_unit + 8 * slot, (k / kUnitSlots) & 1u, p.status, true);
+                if (!ok) break;
+                const int32_t *u = units + slot * 16;
+                const int n_tok = u[5], h = u[1], row0 = u[8];
+                mbar_arrive(bar_unit_free + 8 * slot);
+                if (n_tok <= 0) break;
+                if (k > 0) ok = mbar_wait_bounded(bar_q_free, (k - 1) & 1u, p.status, true);
+                if (!ok) break;
+                mbar_arrive_expect_tx(bar_q, Cfg::Q_BYTES);
 #pragma unroll
-            for (int pn = 0; pn < NP; ++pn)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) o[pn][e][k] = 0.f;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            const uint4 *qr = reinterpret_cast<const uint4 *>(
-                p.q + ((size_t)(u_row0 + r0) * H + u_h) * D + 16 * c);
-#pragma unroll
-            for (int pn = 0; pn < NP; ++pn)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    ql[pn][e] = r0 < u_n ? qr[pn * 8 + e] : zero;
-                    qh[pn][e] = r0 + 8 < u_n ? qr[(size_t)8 * H * (D / 8) + pn * 8 + e] : zero;
-                }
-        }
-        if (mw * 16 < u_n) {
-            const uint32_t kst = ring + st * STAGE + (uint32_t)hw * ((uint32_t)D * 2u << bshift);
-            for (int t0 = 0; t0 < d.w; t0 += 16) {
-                // byte offsets of the chunk's two 8-token groups
-                uint32_t grp[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int t = t0 + 8 * j;
-                    grp[j] = kst + (uint32_t)(t >> bshift) * blk_bytes +
-                             (uint32_t)((t & (B - 1)) >> 3) * (NP * 1024u);
-                }
-                float x[2][4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[j][k] = 0.f;
-#pragma unroll
-                for (int pn = 0; pn < NP; ++pn)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint4 kk = lds128(grp[j] + pn * 1024u + (koff0 ^ (e * 16u)));
-                            mma16816(x[j], ql[pn][e].x, qh[pn][e].x, ql[pn][e].y, qh[pn][e].y, kk.x, kk.y);
-                            mma16816(x[j], ql[pn][e].z, qh[pn][e].z, ql[pn][e].w, qh[pn][e].w, kk.z, kk.w);
-                        }
-                const int pos0 = d.z + t0;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[j][k] *= p.qscale;
-                // drafted positions, or slots past the unit's end (which may hold anything)
-                const bool tail = t0 + 16 > d.w;
-                if (pos0 + 16 > u_base || tail) {
-                    const uint64_t ma = masks[d.x * 64 + r0], mb = masks[d.x * 64 + r0 + 8];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int t = t0 + 8 * j + 2 * c + k, node = d.z + t - u_base;
-                            const bool out = t >= d.w;
-                            if (out || (node >= 0 && !((ma >> node) & 1))) x[j][k] = -INFINITY;
-                            if (out || (node >= 0 && !((mb >> node) & 1))) x[j][2 + k] = -INFINITY;
-                        }
-                }
-                if (SCORES && mw == 0 && g == 0) {
-                    float *sc = p.scores + ((size_t)u_s * H + u_h) * p.score_stride + pos0 + 2 * c;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (t0 + 8 * j + 2 * c < d.w)   // (the stride covers whole blocks)
-                            *reinterpret_cast<float2 *>(sc + 8 * j) = make_float2(x[j][0], x[j][1]);
-                }
-                float n0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-                float n1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
-                n0 = fmaxf(n0, __shfl_xor_sync(kAll, n0, 1));
-                n1 = fmaxf(n1, __shfl_xor_sync(kAll, n1, 1));
-                n0 = fmaxf(n0, __shfl_xor_sync(kAll, n0, 2));
-                n1 = fmaxf(n1, __shfl_xor_sync(kAll, n1, 2));
-                if (__any_sync(kAll, n0 > m0 || n1 > m1)) {
-                    n0 = fmaxf(n0, m0);
-                    n1 = fmaxf(n1, m1);
-                    const float a0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
-                    const float a1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
-                    m0 = n0;
-                    m1 = n1;
-                    l0 *= a0;
-                    l1 *= a1;
-#pragma unroll
-                    for (int pn = 0; pn < NP; ++pn)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            o[pn][e][0] *= a0;
-                            o[pn][e][1] *= a0;
-                            o[pn][e][2] *= a1;
-                            o[pn][e][3] *= a1;
-                        }
-                }
-                // a row that has seen nothing yet keeps m = -inf: its terms are 2^-inf = 0
-                const float f0 = m0 == -INFINITY ? 0.f : m0, f1 = m1 == -INFINITY ? 0.f : m1;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    x[j][0] = ex2(x[j][0] - f0);
-                    x[j][1] = ex2(x[j][1] - f0);
-                    x[j][2] = ex2(x[j][2] - f1);
-                    x[j][3] = ex2(x[j][3] - f1);
-                    l0 += x[j][0] + x[j][1];
-                    l1 += x[j][2] + x[j][3];
-                }
-                const uint32_t a0 = pack_half2(x[0][0], x[0][1]), a1 = pack_half2(x[0][2], x[0][3]);
-                const uint32_t a2 = pack_half2(x[1][0], x[1][1]), a3 = pack_half2(x[1][2], x[1][3]);
-#pragma unroll
-                for (int pn = 0; pn < NP; ++pn) {
-                    uint4 v00 = lds128(grp[0] + HALF + pn * 1024u + voff0);
-                    uint4 v01 = lds128(grp[0] + HALF + pn * 1024u + voff1);
-                    uint4 v10 = lds128(grp[1] + HALF + pn * 1024u + voff0);
-                    uint4 v11 = lds128(grp[1] + HALF + pn * 1024u + voff1);
-                    if (tail) {
-                        const uint4 zero = make_uint4(0, 0, 0, 0);
-                        const int t = t0 + 2 * c;
-                        if (t >= d.w) v00 = zero;
-                        if (t + 1 >= d.w) v01 = zero;
-                        if (t + 8 >= d.w) v10 = zero;
-                        if (t + 9 >= d.w) v11 = zero;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
-                        mma16816(o[pn][e], a0, a1, a2, a3,
-                                 __byte_perm(word_of(v00, e >> 1), word_of(v01, e >> 1), sel),
-                                 __byte_perm(word_of(v10, e >> 1), word_of(v11, e >> 1), sel));
-                    }
-                }
+                for (int pn = 0; pn < NP; ++pn) tma_load_3d(sQ + pn * NQ * 128, &maps.q, pn * 64, h, row0, bar_q);
             }
+            if (!ok) report(p.status, PA_ERR_TIMEOUT);
+            if (k > 0) mbar_wait_bounded(bar_q, (k - 1) & 1u, p.status, false);   // the last copy has landed
         }
         __syncwarp();
+    } else if (warp == kProducts) {
+        // ================================================ products, one thread
+        // Order: S of tile t + 1 before O of tile t, so that the softmax of a
+        // tile finds its S ready; S and P have two buffers, taken in turn.
         if (lane == 0) {
-            mbar_arrive(bar_empty + 8 * st);
-            if (d.y & FLAG_LAST) mbar_arrive(bar_unit + 8 * d.x);
-        }
-        if ((d.y & FLAG_LAST) && mw * 16 < u_n) {
-            l0 += __shfl_xor_sync(kAll, l0, 1);
-            l1 += __shfl_xor_sync(kAll, l1, 1);
-            l0 += __shfl_xor_sync(kAll, l0, 2);
-            l1 += __shfl_xor_sync(kAll, l1, 2);
-            if (u_parts == 1) {
-                const float i0 = 1.f / l0, i1 = 1.f / l1;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {            // rows r0, r0 + 8
-                    if (r0 + 8 * e >= u_n) continue;
-                    const float inv = e ? i1 : i0;
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        p.out + ((size_t)(u_row0 + r0 + 8 * e) * H + u_h) * D + 16 * c);
-#pragma unroll
-                    for (int pn = 0; pn < NP; ++pn)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = pack_half2(o[pn][2 * i][2 * e + k] * inv,
-                                                  o[pn][2 * i + 1][2 * e + k] * inv);
-                            dst[pn * 8 + k] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+            constexpr uint32_t idS = tc::idesc_f16(kTile, NQ, false);
+            constexpr uint32_t idO = tc::idesc_f16(128, NQ, true) | (1u << 15);   // both MN-major
+            int st = 0, st_v = 0;        // stage of the next keys; of the current tile's values
+            uint32_t use = 0, use_v = 0, gs = 0, gp = 0;   // tiles whose S, whose O was issued
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                ok = ok && mbar_wait_bounded(bar, parity, p.status, true);
+                return ok;
+            };
+            auto step = [&](int &i, uint32_t &n) {
+                if (++i == stages) {
+                    i = 0;
+                    ++n;
                 }
-                if (SCORES && lane == 0 && mw == 0)
-                    p.ml_one[(size_t)u_s * H + u_h] = make_float2(m0, l0);
-            } else {
+            };
+            // S (tokens x rows) = K Q^T
+            auto issue_s = [&]() {
+                if (!wait(bar_full + 8 * st, use & 1u)) return;
+                tc::fence_after();
+                const uint64_t dk = tc::smem_desc(ring + st * HALF, 16, 1024u * NP);
+                const uint64_t dq = tc::smem_desc(sQ, 16, 1024);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (r0 + 8 * e >= u_n) continue;
-                    const size_t row = ((size_t)u_gp * H + u_h) * NR + r0 + 8 * e;
-                    if (c == 0) p.ws_ml[row] = e ? make_float2(m1, l1) : make_float2(m0, l0);
-                    float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + row * D + 16 * c);
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc::mma_ss(tmem + Cfg::S_COL + (gs & 1) * NQ,
+                               dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                               dq + (((kk >> 2) * NQ * 128 + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+                tc::commit(bar_empty + 8 * st);
+                tc::commit(bar_s + 8 * (gs & 1));
+                ++gs;
+                step(st, use);
+                step(st, use);
+            };
+            for (uint32_t k = 0;; ++k) {
+                const int slot = k % kUnitSlots;
+                if (!wait(bar_unit + 8 * slot, (k / kUnitSlots) & 1u)) break;
+                const int n_tiles = (units[slot * 16 + 5] + kTile - 1) / kTile;
+                mbar_arrive(bar_unit_free + 8 * slot);
+                if (n_tiles == 0) break;
+                if (!wait(bar_q, k & 1u)) break;
+                issue_s();
+                if (n_tiles == 1) tc::commit(bar_q_free);
+                for (int t = 0; ok && t < n_tiles; ++t) {
+                    step(st_v, use_v);                   // past the keys
+                    if (t + 1 < n_tiles) {
+                        issue_s();
+                        if (t + 2 == n_tiles) tc::commit(bar_q_free);
+                    }
+                    if (!wait(bar_full + 8 * st_v, use_v & 1u) || !wait(bar_p + 8 * (gp & 1), (gp >> 1) & 1u)) break;
+                    tc::fence_after();
+                    // O (dims x rows) += V^T P^T
+                    const uint64_t dv = tc::smem_desc(ring + st_v * HALF, 1024, 1024u * NP);
+                    const uint64_t dp = tc::smem_desc(sP + (gp & 1) * Cfg::P_BYTES, 1024, 1024);
 #pragma unroll
-                    for (int pn = 0; pn < NP; ++pn)
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        tc::mma_ss(tmem + Cfg::O_COL, dv + ((kk * 2048u * NP) >> 4), dp + ((kk * 2048u) >> 4), idO,
+                                   (t > 0 || kk > 0) ? 1u : 0u);
+                    tc::commit(bar_empty + 8 * st_v);
+                    if (t + 1 == n_tiles) tc::commit(bar_o);
+                    ++gp;
+                    step(st_v, use_v);
+                }
+                if (!ok) break;
+            }
+            if (!ok) report(p.status, PA_ERR_TIMEOUT);
+            tc::commit(bar_done);   // lets the teardown wait for every product issued
+        }
+        __syncwarp();
+    } else {
+        // ================================================ softmax warps
+        // Thread = token of the tile (then, for O, dimension of the head).  The
+        // warps go through barriers together: a wait that fails only clears
+        // ok until the next vote.
+        const int tok = tid;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        const float qs = p.qscale;
+        uint32_t g = 0;                                  // tiles so far
+        int st_v = 0;                                    // stage of the tile's values
+        uint32_t use_v = 0;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(kAll, ok && mbar_wait_bounded(bar, parity, p.status, true));
+        };
+        auto step = [&]() {
+            if (++st_v == stages) {
+                st_v = 0;
+                ++use_v;
+            }
+        };
+        // columns [c, c + N) of this thread's lane
+        auto load_cols = [&](uint32_t col, float (&v)[NQ]) {
+            uint32_t r[NQ];
+            if constexpr (NQ == 16) tc::ld16(lane_base + col, r);
+            else if constexpr (NQ == 32) tc::ld32(lane_base + col, r);
+            else tc::ld64(lane_base + col, r);
+            tc::wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
+            for (int i = 0; i < NQ; ++i) v[i] = __uint_as_float(r[i]);
+        };
+        for (uint32_t k = 0;; ++k) {
+            const int slot = k % kUnitSlots;
+            wait(bar_unit + 8 * slot, (k / kUnitSlots) & 1u);
+            if (!softmax_all(ok)) break;
+            const int32_t *u = units + slot * 16;
+            const int s = u[0], h = u[1], part = u[2], parts = u[3], tok_first = u[4], n_tok = u[5], base = u[6],
+                      n = u[7], row0 = u[8];
+            if (n_tok <= 0) break;                       // the end
+            float l[R];
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                dst[pn * 16 + k * 2 + i] =
-                                    make_float4(o[pn][4 * i][2 * e + k], o[pn][4 * i + 1][2 * e + k],
-                                                o[pn][4 * i + 2][2 * e + k], o[pn][4 * i + 3][2 * e + k]);
+            for (int i = 0; i < R; ++i) l[i] = 0.f;
+            for (int t0 = 0; t0 < n_tok; t0 += kTile) {
+                const int nv = min(kTile, n_tok - t0);
+                step();                                  // past the keys' stage
+                wait(bar_s + 8 * (g & 1), (g >> 1) & 1u);
+                tc::fence_after();
+                float y[NQ];
+                load_cols(Cfg::S_COL + (g & 1) * NQ, y);
+                const int pos = tok_first + t0 + tok;
+#pragma unroll
+                for (int i = 0; i < R; ++i) y[i] *= qs;
+                if (tok_first + t0 + kTile > base || nv < kTile) {
+                    // who sees this position: every row before the nodes, then
+                    // the node itself and its descendants; none past the end
+                    const uint64_t v = tok >= nv ? 0ull : pos < base ? ~0ull : seen[slot * 64 + pos - base];
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        if (!((v >> i) & 1)) y[i] = -INFINITY;
+                }
+                if (SCORES && tok < nv) p.scores[((size_t)s * H + h) * p.score_stride + pos] = y[0];
+                // a row's reference moves when a score passes it by more than 2^8
+                bool over = t0 == 0;
+                if (t0 > 0) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < G; ++c) {
+                        if (8 * c >= n) break;
+                        float f[8];
+                        load8(ref + 8 * c, f);
+#pragma unroll
+                        for (int e = 0; e < (SCORES ? 1 : 8); ++e) top = fmaxf(top, y[8 * c + e] - f[e]);
+                    }
+                    over = top > kRescaleLog2;
+                }
+                if (softmax_any(over || !ok)) {
+                    if (!softmax_all(ok)) break;
+                    float m[R];
+#pragma unroll
+                    for (int i = 0; i < R; ++i) m[i] = y[i];
+                    const int first = warp_combine(m, lane, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+                    for (int i = 0; i < (R + 31) / 32; ++i) red[warp * NQ + first + i] = m[i];
+                    softmax_sync();
+                    if (tid < R) {
+                        float top = red[tid];
+#pragma unroll
+                        for (int w = 1; w < kSoftmaxWarps; ++w) top = fmaxf(top, red[w * NQ + tid]);
+                        // (a row that has seen nothing yet has reference -2^100: its
+                        // terms, if any come, are rescaled from 0)
+                        const float old = t0 ? ref[tid] : -0x1p100f, now = top > old + kRescaleLog2 ? top : old;
+                        ref[tid] = now;
+                        corr[tid] = ex2(old - now);
+                    }
+                    softmax_sync();
+                    if (t0 > 0) {
+#pragma unroll
+                        for (int i = 0; i < R; ++i) l[i] *= corr[i];
+                        // O up to the tile before: its product gave the values' stage back
+                        const int ps = st_v >= 2 ? st_v - 2 : st_v - 2 + stages;
+                        wait(bar_empty + 8 * ps, (st_v >= 2 ? use_v : use_v - 1) & 1u);
+                        tc::fence_after();
+                        float o[NQ];
+                        load_cols(Cfg::O_COL, o);
+#pragma unroll
+                        for (int i = 0; i < R; ++i) o[i] *= corr[i];
+                        uint32_t r[NQ];
+#pragma unroll
+                        for (int i = 0; i < NQ; ++i) r[i] = __float_as_uint(o[i]);
+                        if constexpr (NQ == 16) tc::st16(lane_base + Cfg::O_COL, r);
+                        else if constexpr (NQ == 32) tc::st32(lane_base + Cfg::O_COL, r);
+                        else tc::st64(lane_base + Cfg::O_COL, r);
+                        tc::wait_st();
+                    }
+                }
+                // P of the tile: this token's row, in the second operand's layout
+                const uint32_t prow = sP + (g & 1) * Cfg::P_BYTES + (uint32_t)tok * 128u;
+#pragma unroll
+                for (int c = 0; c < G; ++c) {
+                    if (8 * c >= n) break;
+                    float f[8];
+                    load8(ref + 8 * c, f);
+                    uint32_t w[4] = {0, 0, 0, 0};
+                    if constexpr (SCORES) {
+                        const float p0 = ex2(y[0] - f[0]);
+                        l[0] += p0;
+                        w[0] = pack_half2(p0, 0.f);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = 8 * c + 2 * e;
+                            const float p0 = ex2(y[i] - f[2 * e]), p1 = ex2(y[i + 1] - f[2 * e + 1]);
+                            l[i] += p0;
+                            l[i + 1] += p1;
+                            w[e] = pack_half2(p0, p1);
+                        }
+                    }
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     prow + (uint32_t)((c ^ (tok & 7)) << 4)),
+                                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                }
+                if (nv < kTile) {
+                    // values past the end meet P = 0 and have to be finite: zeros
+                    wait(bar_full + 8 * st_v, use_v & 1u);
+                    if (tok >= nv) {
+                        const uint32_t row = ring + st_v * HALF + (uint32_t)(tok >> 3) * (NP * 1024u) +
+                                             (uint32_t)(tok & 7) * 128u;
+#pragma unroll
+                        for (int c = 0; c < NP * 8; ++c)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             row + (uint32_t)(c >> 3) * 1024u + (uint32_t)(c & 7) * 16u),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                }
+                fence_proxy_async_smem();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_p + 8 * (g & 1));
+                ++g;
+                step();
+            }
+            if (!softmax_all(ok)) break;
+            if (lane == 0) mbar_arrive(bar_unit_free + 8 * slot);
+            // sums over the tokens
+            const int first = warp_combine(l, lane, [](float a, float b) { return a + b; });
+#pragma unroll
+            for (int i = 0; i < (R + 31) / 32; ++i) red[warp * NQ + first + i] = l[i];
+            softmax_sync();
+            const size_t part_row = ((size_t)part * H + h) * NQ;
+            if (tid < R) {
+                float sum = red[tid];
+#pragma unroll
+                for (int w = 1; w < kSoftmaxWarps; ++w) sum += red[w * NQ + tid];
+                corr[tid] = 1.f / sum;
+                if (parts > 1 && tid < n) p.ws_ml[part_row + tid] = make_float2(ref[tid], sum);
+                if (SCORES && parts == 1) p.ml_one[(size_t)s * H + h] = make_float2(ref[0], sum);
+            }
+            softmax_sync();
+            wait(bar_o, k & 1u);
+            tc::fence_after();
+            float o[NQ];
+            load_cols(Cfg::O_COL, o);
+            if (tok < D) {                               // thread = dimension
+                if (parts == 1) {
+                    __half *dst = p.out + ((size_t)row0 * H + h) * D + tok;
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        if (i < n) dst[(size_t)i * H * D] = __float2half(o[i] * corr[i]);
+                } else {
+                    float *dst = p.ws_acc + part_row * D + tok;
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        if (i < n) dst[i * D] = o[i];
                 }
             }
+            __syncwarp();
         }
-        if (++st == stages) {
-            st = 0;
-            ++use;
-        }
+        if (!ok && lane == 0) report(p.status, PA_ERR_TIMEOUT);
+        __syncwarp();
+    }
+
+    // ---- teardown: every product drained (bounded), then tensor memory freed
+    tc::fence_before();
+    __syncthreads();
+    if (warp == kProducts) {
+        if (lane == 0 && !mbar_wait_bounded(bar_done, 0, p.status, false)) report(p.status, PA_ERR_TIMEOUT);
+        __syncwarp();
+        tc::fence_after();
+        tc::dealloc(tmem, Cfg::COLS);
     }
 }
 
@@ -855,7 +1066,7 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
 }
 
 // A cache as [row / 8][panel][row % 8][64] fp16 with a box of one block's
-// rows of GH adjacent heads.
+// rows of one head.
 int encode_cache(CUtensorMap *m, const void *base, int64_t groups, int D, int box_groups, const char *who) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
     if (!enc) return fail(PA_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", who);
@@ -863,6 +1074,20 @@ int encode_cache(CUtensorMap *m, const void *base, int64_t groups, int D, int bo
     const cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16};
     const cuuint32_t box[4] = {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)box_groups}, elem[4] = {1, 1, 1, 1};
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), dims, strides, box,
+                           elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", who, (int)r);
+    return PA_OK;
+}
+
+// Queries as [rows][H][D] with a box of 64 columns of one head of box_rows rows.
+int encode_queries(CUtensorMap *m, const void *base, int rows, int H, int D, int box_rows, const char *who) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
+    if (!enc) return fail(PA_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", who);
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, elem[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides, box,
                            elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", who, (int)r);
@@ -883,24 +1108,15 @@ int sm_count() {
     return n[dev];
 }
 
-// Heads a unit takes: as many adjacent ones as divide H (longer copies), at
-// most 4, 2 with 64 query rows (8 consumer warps) and 2 where a stage of 4
-// heads would be 64 KB (D = 128, B = 32).
-int heads_per_unit(int H, int MW, int D, int B) {
-    int gh = H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
-    if (MW == 4 || (D == 128 && B == 32)) gh = std::min(gh, 2);
-    return gh;
-}
-int row_tiles(int max_q) { return max_q <= 16 ? 1 : max_q <= 32 ? 2 : 4; }
+// Query rows of a launch, padded to what a product's N takes.
+int padded_rows(int max_q) { return max_q <= 16 ? 16 : max_q <= 32 ? 32 : 64; }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Parts of cut sequences a launch can have: each is at least half a slot's
-// share of the blocks, rounded up, and a sequence of k > 1 parts is longer
-// than k - 1 of them; at most 4 CTAs an SM take units.
-int part_cap(int n_seqs, int max_blocks, int hg) {
-    const int64_t slots = (int64_t)sm_count() * 4;
-    return (int)std::min<int64_t>(4 * slots / hg + 4, (int64_t)n_seqs * std::max(max_blocks, 1));
+// Parts of cut sequences a launch can have: each is at least half of a
+// quarter of an SM's share of the blocks.
+int part_cap(int n_seqs, int max_blocks, int H) {
+    return (int)std::min<int64_t>(8ll * sm_count() / H + 8, (int64_t)n_seqs * std::max(max_blocks, 1));
 }
 
 struct Sections {
@@ -945,55 +1161,38 @@ bool tree_geometry_ok(const pa_pool_desc *d, std::string *why) {
     return true;
 }
 
-template <int D, int GH, int MW, bool SCORES>
+template <int D, int NQ, bool SCORES>
 int launch_tree(TreeParams p, const TreeMaps &maps, const char *who, cudaStream_t st) {
-    using Cfg = TreeCfg<D, GH, MW>;
-    auto kern = tree_attention_kernel<D, GH, MW, SCORES>;
-    constexpr int kSmBytes = 227 * 1024, kMaxBytes = 227 * 1024;
+    using Cfg = TreeCfg<D, NQ>;
+    auto kern = tree_attention_kernel<D, NQ, SCORES>;
+    constexpr int kBytes = 227 * 1024;
     static std::once_flag once[kMaxDevs];
     static cudaError_t err[kMaxDevs];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevs)
         return fail(PA_ERR_CUDA, "%s: cudaGetDevice failed", who);
     std::call_once(once[dev], [&] {
-        err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBytes);
+        err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     });
     if (err[dev] != cudaSuccess)
         return fail(PA_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(err[dev]));
-    // as many CTAs an SM as leave each at least 3 stages beside its plan
-    int per_sm = Cfg::PER_SM, stages = 0;
-    // a stage holds whole blocks, 16 tokens at least, and 16 KB
-    p.stage_tokens = std::max(std::max(16, 1 << p.bshift), 16384 / (GH * D * 4));
-    const int stage_bytes = GH * p.stage_tokens * D * 4;
-    for (; per_sm >= 1; --per_sm) {
-        const int room = (per_sm == 1 ? kMaxBytes : (kSmBytes + 1024) / per_sm - 1024) - Cfg::bytes(p.n_seqs, 0);
-        stages = std::min(Cfg::MAX_STAGES, room / stage_bytes);
-        if (stages >= 3) break;
-    }
-    if (per_sm < 1) return fail(PA_ERR_INVALID_ARG, "%s: the batch's plan does not fit", who);
-    p.stages = stages;
+    p.stages = std::min(kMaxStages, (kBytes - Cfg::bytes(p.n_seqs, 0)) / Cfg::HALF);
+    static_assert((227 * 1024 - TreeCfg<128, 64>::PLAN - 10 * PA_TREE_MAX_SEQS - 8 - 1024 - TreeCfg<128, 64>::Q_BYTES -
+                   2 * TreeCfg<128, 64>::P_BYTES) / TreeCfg<128, 64>::HALF >= kMinStages,
+                  "room beside the largest batch's plan");
     cudaError_t e = cudaMemsetAsync(p.header, 0, 8, st);
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: memset: %s", who, cudaGetErrorString(e));
-    kern<<<sm_count() * per_sm, Cfg::THREADS, Cfg::bytes(p.n_seqs, stages * stage_bytes), st>>>(p, maps);
+    kern<<<sm_count(), kThreads, Cfg::bytes(p.n_seqs, p.stages), st>>>(p, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return PA_OK;
 }
 
-template <int D, int MW, bool SCORES>
-int launch_heads(int gh, const TreeParams &p, const TreeMaps &maps, const char *who, cudaStream_t st) {
-    if constexpr (MW < 4)
-        if (gh == 4) return launch_tree<D, 4, MW, SCORES>(p, maps, who, st);
-    if (gh == 2) return launch_tree<D, 2, MW, SCORES>(p, maps, who, st);
-    return launch_tree<D, 1, MW, SCORES>(p, maps, who, st);
-}
-
 // Checks and the main launch that both entry points share.
 int launch_common(const char *who, bool weights, TreeParams &p, const void *k_cache, const void *v_cache,
                   void *workspace, size_t workspace_bytes, int max_q, const pa_pool_desc *d, cudaStream_t st) {
-    const int MW = row_tiles(max_q), NR = 16 * MW, B = d->block_size;
-    const int gh = heads_per_unit(d->num_heads, MW, d->head_dim, B);
-    p.cap = part_cap(p.n_seqs, p.max_blocks, d->num_heads / gh);
+    const int NR = padded_rows(max_q), B = d->block_size;
+    p.cap = part_cap(p.n_seqs, p.max_blocks, d->num_heads);
     const Sections s = sections(p.n_seqs, p.max_blocks, NR, p.cap, weights, d);
     if (!workspace || workspace_bytes < s.total)
         return fail(PA_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, %zu given", who, s.total,
@@ -1017,19 +1216,20 @@ int launch_common(const char *who, bool weights, TreeParams &p, const void *k_ca
     p.max_q = max_q;
     TreeMaps maps;
     const int64_t groups = (int64_t)d->num_blocks * d->num_heads * B / 8;
-    int rc = encode_cache(&maps.k, k_cache, groups, d->head_dim, gh * B / 8, who);
-    if (rc == PA_OK) rc = encode_cache(&maps.v, v_cache, groups, d->head_dim, gh * B / 8, who);
+    int rc = encode_cache(&maps.k, k_cache, groups, d->head_dim, B / 8, who);
+    if (rc == PA_OK) rc = encode_cache(&maps.v, v_cache, groups, d->head_dim, B / 8, who);
+    if (rc == PA_OK) rc = encode_queries(&maps.q, p.q, p.q_rows, d->num_heads, d->head_dim, NR, who);
     if (rc != PA_OK) return rc;
     if (d->head_dim == 64) {
-        if (weights) return launch_heads<64, 1, true>(gh, p, maps, who, st);
-        return MW == 1 ? launch_heads<64, 1, false>(gh, p, maps, who, st)
-             : MW == 2 ? launch_heads<64, 2, false>(gh, p, maps, who, st)
-                       : launch_heads<64, 4, false>(gh, p, maps, who, st);
+        if (weights) return launch_tree<64, 16, true>(p, maps, who, st);
+        return NR == 16 ? launch_tree<64, 16, false>(p, maps, who, st)
+             : NR == 32 ? launch_tree<64, 32, false>(p, maps, who, st)
+                        : launch_tree<64, 64, false>(p, maps, who, st);
     }
-    if (weights) return launch_heads<128, 1, true>(gh, p, maps, who, st);
-    return MW == 1 ? launch_heads<128, 1, false>(gh, p, maps, who, st)
-         : MW == 2 ? launch_heads<128, 2, false>(gh, p, maps, who, st)
-                   : launch_heads<128, 4, false>(gh, p, maps, who, st);
+    if (weights) return launch_tree<128, 16, true>(p, maps, who, st);
+    return NR == 16 ? launch_tree<128, 16, false>(p, maps, who, st)
+         : NR == 32 ? launch_tree<128, 32, false>(p, maps, who, st)
+                    : launch_tree<128, 64, false>(p, maps, who, st);
 }
 
 bool mis(const void *ptr, int n) { return (reinterpret_cast<uintptr_t>(ptr) & (n - 1)) != 0; }
@@ -1041,16 +1241,14 @@ size_t tree_workspace_bytes(int32_t n_seqs, int32_t max_blocks, int32_t max_q_le
     if (!d || n_seqs <= 0 || n_seqs > PA_TREE_MAX_SEQS || max_blocks < 0 || max_q_len < 1 ||
         max_q_len > PA_TREE_MAX_NODES || !tree_geometry_ok(d, &why))
         return 0;
-    const int MW = row_tiles(max_q_len);
-    const int hg = d->num_heads / heads_per_unit(d->num_heads, MW, d->head_dim, d->block_size);
-    return sections(n_seqs, max_blocks, 16 * MW, part_cap(n_seqs, max_blocks, hg), false, d).total;
+    return sections(n_seqs, max_blocks, padded_rows(max_q_len), part_cap(n_seqs, max_blocks, d->num_heads), false, d)
+        .total;
 }
 
 size_t decode_weights_workspace_bytes(int32_t n_seqs, int32_t max_blocks, const pa_pool_desc *d) {
     std::string why;
     if (!d || n_seqs <= 0 || n_seqs > PA_TREE_MAX_SEQS || max_blocks < 0 || !tree_geometry_ok(d, &why)) return 0;
-    const int hg = d->num_heads / heads_per_unit(d->num_heads, 1, d->head_dim, d->block_size);
-    return sections(n_seqs, max_blocks, 16, part_cap(n_seqs, max_blocks, hg), true, d).total;
+    return sections(n_seqs, max_blocks, padded_rows(1), part_cap(n_seqs, max_blocks, d->num_heads), true, d).total;
 }
 
 int launch_tree_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -1091,7 +1289,7 @@ int launch_tree_attention(void *out, const void *q, const void *k_cache, const v
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int rc = launch_common(who, false, p, k_cache, v_cache, workspace, workspace_bytes, max_q_len, d, st);
     if (rc != PA_OK) return rc;
-    const int NR = 16 * row_tiles(max_q_len);
+    const int NR = padded_rows(max_q_len);
     const int blocks = (int)std::min<int64_t>((int64_t)p.cap * d->num_heads * NR / 8 + 1, (int64_t)sm_count() * 4);
     if (d->head_dim == 64) tree_join_kernel<64><<<blocks, 256, 0, st>>>(p, NR);
     else tree_join_kernel<128><<<blocks, 256, 0, st>>>(p, NR);
@@ -1139,7 +1337,7 @@ int launch_decode_attention_weights(void *out, float *weights_out, const float *
     const int rc = launch_common(who, true, p, k_cache, v_cache, workspace, workspace_bytes, 1, d, st);
     if (rc != PA_OK) return rc;
     const bool vec = weight_len % 4 == 0 && !mis(weights_out, 16) && !mis(weights_in, 16);
-    auto go = [&](auto kern) { kern<<<grid, 256, 0, st>>>(p, 16, weights_out, weights_in); };
+    auto go = [&](auto kern) { kern<<<grid, 256, 0, st>>>(p, padded_rows(1), weights_out, weights_in); };
     if (d->head_dim == 64) vec ? go(decode_weights_kernel<64, true>) : go(decode_weights_kernel<64, false>);
     else vec ? go(decode_weights_kernel<128, true>) : go(decode_weights_kernel<128, false>);
     const cudaError_t e = cudaGetLastError();

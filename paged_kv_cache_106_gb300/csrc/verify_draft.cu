@@ -17,10 +17,11 @@
 // Exactness.  A running sum crosses an edge at every token, so rounding of
 // 2^-24 in it would move the answer once in some hundred samples at 50 k
 // tokens.  All weights are therefore pairs of fp32 (value + error term, 2^-48),
-// added with error-free transformations; per-thread sums join in fp64, a few
-// adds a thread (in fp64 alone the row's additions would take three times the
-// time of its bytes on this GPU).  No atomics: the result depends only on the
-// inputs.
+// added with error-free transformations; only the joining of the warps' sums
+// and the tests of single tokens are in fp64, in one warp (this GPU does two
+// fp64 operations a clock and SM: with sums joined in fp64 by every thread
+// 256 rows of 50 k tokens took 342 us, this way ...).  No atomics: the result depends
+// only on the inputs.
 //
 // What bounds it: the rows it has to read (one target row, and one draft row
 // once something is rejected, 4 V bytes each) for a large batch; the chain of
@@ -46,6 +47,7 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
+static_assert(kMaxCluster * kWarps <= 64, "a lane of warp 0 takes two warps' sums");
 constexpr int kNodes = PA_TREE_MAX_NODES;
 
 struct VerifyParams {
@@ -58,13 +60,25 @@ struct VerifyParams {
 };
 
 // A nonnegative weight as an unevaluated sum of two fp32.
-struct Pair {
+struct __align__(8) Pair {
     float hi, lo;
 };
 
 __device__ __forceinline__ Pair two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
     return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+    Pair t = two_sum(a.hi, b.hi);
+    const float lo = __fadd_rn(t.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(t.hi, lo);
+    return {hi, __fsub_rn(lo, __fsub_rn(hi, t.hi))};
+}
+
+__device__ __forceinline__ bool above(Pair a, Pair b) {
+    if (b.hi == INFINITY) return false;
+    const Pair d = two_sum(a.hi, -b.hi);
+    return __fadd_rn(d.hi, __fadd_rn(d.lo, __fsub_rn(a.lo, b.lo))) > 0.f;
 }
 
 // max(w - z q, 0), z = zh + zl
@@ -123,12 +137,12 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ double load_cluster(const double *local, uint32_t rank) {
+__device__ __forceinline__ double load_cluster(const Pair *local, uint32_t rank) {
     uint32_t a;
-    double v;
+    Pair v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a) : "memory");
-    return v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.hi), "=f"(v.lo) : "r"(a) : "memory");
+    return (double)v.hi + (double)v.lo;
 }
 
 struct Shared {
@@ -136,9 +150,12 @@ struct Shared {
     int32_t up[kNodes], tok[kNodes];
     float zh[kNodes], zl[kNodes];              // Z before each rejection at the current node
     int32_t out[kNodes];                       // the tokens rejected there
-    double wsum[2][kWarps];                    // this CTA's warps' sums, by parity of the pass
-    double all[kMaxCluster * kWarps];          // every warp's sums, in order of index
+    Pair wsum[2][kWarps];                      // this CTA's warps' sums, by parity of the pass
+    int32_t cur, k;                            // the row to add up: its node, rejections there
+    int32_t owner;                             // the warp that finds the next token, or:
+    Pair left;                                 // of the target, within the owner's span
 };
+enum { kAgain = -1, kNone = -2 };
 
 template <typename T, bool DRAFT, int VEC>
 __global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyParams a) {
@@ -220,139 +237,156 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyPara
             }
         }
     };
-    // Sums of the row's weights by warp into sh.all (of the whole cluster);
-    // returns their total, added in order of index (the same in every CTA).
-    int parity = 0;
-    auto row_sums = [&](int v, int k) {
-        float acc = 0.f, err = 0.f;
-#pragma unroll 4
-        for (int i = lo + lane * VEC; i < hi; i += 32 * VEC) {
-            Pair w[VEC];
-            weights(v, k, i, w);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const Pair t = two_sum(acc, w[e].hi);
-                acc = t.hi;
-                err = __fadd_rn(err, __fadd_rn(t.lo, w[e].lo));
-            }
-        }
-        double sum = (double)acc + (double)err;
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
-        if (lane == 0) sh.wsum[parity][warp] = sum;
-        cluster_sync();
-        if (tid < (int)C * kWarps)
-            sh.all[tid] = load_cluster(&sh.wsum[parity][tid % kWarps], (uint32_t)(tid / kWarps));
-        __syncthreads();
-        parity ^= 1;
-        double total = 0.;
-        for (int i = 0; i < (int)C * kWarps; ++i) total += sh.all[i];
-        return total;
-    };
 
-    // ---- the walk (every thread alike)
-    int cur = 0, k = 0, len = 1;
+    // Warp 0 of every CTA walks (alike, in fp64: a few operations a node; the
+    // other warps would only queue for the fp64 unit) up to where the sum of a
+    // row is needed, all warps add up that row, warp 0 goes on.
+    int i = 1, cur = 0, k = 0, len = 1;
     bool pending = false;       // the last rejection's sum is not known yet
     double z = 1.;
     int32_t *path = a.path + (size_t)s * a.max_q;
     const bool writer = rank == 0 && tid == 0;
     if (writer) path[0] = 0;
-    for (int i = 1; i < n; ++i) {
-        if (sh.up[i] != cur) continue;
-        if (pending) {
-            const double total = row_sums(cur, k);
-            if (total > 0.) z = total; else --k;
-            pending = false;
-        }
-        Pair w = {sh.pu[i], 0.f};
-        const float qx = sh.qu[i];
-        if (DRAFT) {
-            for (int r = 0; r < k; ++r) w = reject(w, qx, sh.zh[r], sh.zl[r]);
-        } else {
-            for (int r = 0; r < k; ++r)
-                if (sh.out[r] == sh.tok[i]) w = {0.f, 0.f};
-        }
-        // (u q is exact in fp64)
-        if ((double)sh.u[i] * (double)qx * z < (double)w.hi + (double)w.lo) {
-            cur = i;
-            k = 0;
-            z = 1.;
-            if (writer) path[len] = i;
-            ++len;
-        } else {
-            __syncthreads();    // every thread has read the list's earlier entries
-            if (tid == 0) {
-                sh.zh[k] = (float)z;
-                sh.zl[k] = (float)(z - (double)(float)z);
-                sh.out[k] = sh.tok[i];
+    for (int parity = 0;; parity ^= 1) {
+        if (warp == 0) {
+            for (; i < n; ++i) {
+                if (sh.up[i] != cur) continue;
+                if (pending) break;
+                Pair w = {sh.pu[i], 0.f};
+                const float qx = sh.qu[i];
+                if (DRAFT) {
+                    for (int r = 0; r < k; ++r) w = reject(w, qx, sh.zh[r], sh.zl[r]);
+                } else {
+                    for (int r = 0; r < k; ++r)
+                        if (sh.out[r] == sh.tok[i]) w = {0.f, 0.f};
+                }
+                // (u q is exact in fp64)
+                if ((double)sh.u[i] * (double)qx * z < (double)w.hi + (double)w.lo) {
+                    cur = i;
+                    k = 0;
+                    z = 1.;
+                    if (writer) path[len] = i;
+                    ++len;
+                } else {
+                    __syncwarp();       // every lane has read the list's earlier entries
+                    if (lane == 0) {
+                        sh.zh[k] = (float)z;
+                        sh.zl[k] = (float)(z - (double)(float)z);
+                        sh.out[k] = sh.tok[i];
+                    }
+                    __syncwarp();
+                    ++k;
+                    pending = true;
+                }
             }
-            __syncthreads();
-            ++k;
-            pending = true;
+            if (lane == 0) {
+                sh.cur = cur;
+                sh.k = k;
+            }
         }
-    }
-    double total = row_sums(cur, k);
-    if (pending && !(total > 0.)) total = row_sums(cur, --k);
+        __syncthreads();
+        const int v = sh.cur, kk = sh.k;
+        Pair acc = {0.f, 0.f};
+#pragma unroll 4
+        for (int x = lo + lane * VEC; x < hi; x += 32 * VEC) {
+            Pair w[VEC];
+            weights(v, kk, x, w);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const Pair t = two_sum(acc.hi, w[e].hi);
+                acc = {t.hi, __fadd_rn(acc.lo, __fadd_rn(t.lo, w[e].lo))};
+            }
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            acc = add(acc, {__shfl_xor_sync(kAll, acc.hi, off), __shfl_xor_sync(kAll, acc.lo, off)});
+        if (lane == 0) sh.wsum[parity][warp] = acc;
+        cluster_sync();
+        if (warp == 0) {
+            // lane l: the sums of warps 2l and 2l + 1 of the row
+            double w0 = 0., w1 = 0.;
+            const int g0 = 2 * lane, g1 = g0 + 1, all = (int)C * kWarps;
+            if (g0 < all) w0 = load_cluster(&sh.wsum[parity][g0 % kWarps], (uint32_t)(g0 / kWarps));
+            if (g1 < all) w1 = load_cluster(&sh.wsum[parity][g1 % kWarps], (uint32_t)(g1 / kWarps));
+            double incl = w0 + w1;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const double y = __shfl_up_sync(kAll, incl, off);
+                if (lane >= off) incl += y;
+            }
+            const double total = __shfl_sync(kAll, incl, 31);
+            int owner = kAgain;
+            if (pending && !(total > 0.)) {      // nothing would be left: the weights stay
+                --k;
+                pending = false;
+            } else if (i < n) {                  // on with the next child
+                if (pending) z = total;
+                pending = false;
+            } else if (!(total > 0.)) {
+                owner = kNone;
+                if (writer) report(a.status, PA_ERR_INVALID_ARG);
+            } else {
+                // the warp whose span the target falls into finds the token
+                const double target = (double)us * total, before = incl - (w0 + w1);
+                const unsigned m0 = __ballot_sync(kAll, before + w0 > target);
+                const unsigned m1 = __ballot_sync(kAll, incl > target);
+                const unsigned p0 = __ballot_sync(kAll, w0 > 0.), p1 = __ballot_sync(kAll, w1 > 0.);
+                const int f0 = m0 ? 2 * (__ffs(m0) - 1) : INT_MAX, f1 = m1 ? 2 * (__ffs(m1) - 1) + 1 : INT_MAX;
+                owner = min(f0, f1);
+                const bool past = owner == INT_MAX;   // the target rounds to the total or more
+                if (past)
+                    owner = max(p0 ? 2 * (31 - __clz(p0)) : 0, p1 ? 2 * (31 - __clz(p1)) + 1 : 0);
+                if (lane == owner / 2) {
+                    const double left = past ? INFINITY : target - (owner & 1 ? before + w0 : before);
+                    sh.left = {(float)left, past ? 0.f : (float)(left - (double)(float)left)};
+                }
+            }
+            if (lane == 0) sh.owner = owner;
+        }
+        __syncthreads();
+        if (sh.owner == kAgain) continue;
 
-    // ---- the next token: the warp whose span the target falls into finds it
-    if (writer) a.path_lens[s] = len;
-    if (rank == 0)
-        for (int i = len + tid; i < a.max_q; i += kThreads) path[i] = -1;
-    if (!(total > 0.)) {
         if (writer) {
-            a.next_tokens[s] = -1;
-            report(a.status, PA_ERR_INVALID_ARG);
+            a.path_lens[s] = len;
+            if (sh.owner == kNone) a.next_tokens[s] = -1;
         }
-    } else {
-        const double target = (double)us * total;
-        int owner = -1, last = 0;
-        double before = 0., run = 0.;
-        for (int i = 0; i < (int)C * kWarps; ++i) {
-            const double w = sh.all[i];
-            if (w > 0.) last = i;
-            if (owner < 0 && run + w > target) {
-                owner = i;
-                before = run;
-            }
-            run += w;
-        }
-        const bool past = owner < 0;       // the target rounds to the total or more
-        if (past) owner = last;
-        if (gw == owner) {
+        if (rank == 0 && warp == 0)
+            for (int x = len + lane; x < a.max_q; x += 32) path[x] = -1;
+        if (gw == sh.owner) {
+            // the first token at which the span's running sum passes what is left
+            const Pair left = sh.left;
             int found = INT_MAX, positive = -1;
-            double base = before;
-            for (int i0 = lo; i0 < hi && found == INT_MAX; i0 += 32 * VEC) {
-                const int i = i0 + lane * VEC;
-                Pair w[VEC];
+            Pair base = {0.f, 0.f};
+            for (int x0 = lo; x0 < hi && found == INT_MAX; x0 += 32 * VEC) {
+                const int x = x0 + lane * VEC;
+                Pair w[VEC], run[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) w[e] = {0.f, 0.f};
-                if (i < hi) weights(cur, k, i, w);
-                double mine[VEC], sum = 0.;
+                if (x < hi) weights(v, kk, x, w);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    sum += (double)w[e].hi + (double)w[e].lo;
-                    mine[e] = sum;
-                    if (w[e].hi > 0.f) positive = i + e;
+                    run[e] = e ? add(run[e - 1], w[e]) : w[e];
+                    if (w[e].hi > 0.f) positive = x + e;
                 }
-                double incl = sum;
+                Pair incl = run[VEC - 1];
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
-                    const double y = __shfl_up_sync(kAll, incl, off);
-                    if (lane >= off) incl += y;
+                    const Pair y = {__shfl_up_sync(kAll, incl.hi, off), __shfl_up_sync(kAll, incl.lo, off)};
+                    if (lane >= off) incl = add(incl, y);
                 }
-                const double excl = base + (incl - sum);
-                if (!past) {
+                Pair excl = {__shfl_up_sync(kAll, incl.hi, 1), __shfl_up_sync(kAll, incl.lo, 1)};
+                excl = lane == 0 ? base : add(base, excl);
 #pragma unroll
-                    for (int e = VEC - 1; e >= 0; --e)
-                        if (w[e].hi > 0.f && excl + mine[e] > target) found = i + e;
-                }
-                base += __shfl_sync(kAll, incl, 31);
+                for (int e = VEC - 1; e >= 0; --e)
+                    if (w[e].hi > 0.f && above(add(excl, run[e]), left)) found = x + e;
+                base = add(base, {__shfl_sync(kAll, incl.hi, 31), __shfl_sync(kAll, incl.lo, 31)});
                 found = __reduce_min_sync(kAll, found);
             }
             positive = __reduce_max_sync(kAll, positive);
             // (rounding can leave the last element short of the warp's sum)
             if (lane == 0) a.next_tokens[s] = found != INT_MAX ? found : positive;
         }
+        break;
     }
     cluster_sync();   // no CTA leaves while another may read its sums
 }
