@@ -45,6 +45,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <mutex>
 
@@ -55,7 +56,7 @@
 namespace pagedkv {
 
 namespace tc {
-// 16 or 64 consecutive 32-bit columns of this thread's lane.
+// 16 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -64,41 +65,6 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
           "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
-}
-__device__ __forceinline__ void ld64(uint32_t taddr, uint32_t (&r)[64]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,"
-        "%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,"
-        "%62,%63}, [%64];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]),
-          "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
-          "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
-          "=r"(r[63])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void st64(uint32_t taddr, const uint32_t (&r)[64]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,"
-        "%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,"
-        "%61,%62,%63,%64};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-          "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-          "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-          "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(r[32]), "r"(r[33]), "r"(r[34]), "r"(r[35]),
-          "r"(r[36]), "r"(r[37]), "r"(r[38]), "r"(r[39]), "r"(r[40]), "r"(r[41]), "r"(r[42]),
-          "r"(r[43]), "r"(r[44]), "r"(r[45]), "r"(r[46]), "r"(r[47]), "r"(r[48]), "r"(r[49]),
-          "r"(r[50]), "r"(r[51]), "r"(r[52]), "r"(r[53]), "r"(r[54]), "r"(r[55]), "r"(r[56]),
-          "r"(r[57]), "r"(r[58]), "r"(r[59]), "r"(r[60]), "r"(r[61]), "r"(r[62]), "r"(r[63])
-        : "memory");
 }
 }  // namespace tc
 
@@ -168,6 +134,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// Lets the kernel launched after this one start (it then waits, at
+// wait_for_launch_before, for this one's end).
+__device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Rows and length of sequence s; 0 rows: nothing to do (or refused, reported).
 struct SeqRows {
     int n, row0, ctx;
@@ -208,6 +179,26 @@ __device__ __forceinline__ int warp_incl_scan(int v, int lane) {
     return v;
 }
 
+// How many tiles a part may have.  A unit costs its tiles, about one more to
+// get going, and where it is a part of a cut sequence the writing and joining
+// of its rows.  Every lane brings a candidate: the longest sequence in
+// lane + 1 parts, and how many units (before heads) and parts that makes.
+__device__ __forceinline__ int part_size(const TreeParams &p, long long total, int longest, int some, int HG,
+                                         int mine, int units_n, int cuts, int lane) {
+    const int slots = gridDim.x, extra = kTile + 2 * p.max_q;     // in tokens
+    // many units: parts of a quarter of an SM's share
+    if ((long long)some * HG >= 4 * slots) return max(1, (int)((total * HG + 4 * slots - 1) / (4 * slots)));
+    // few: by what the last SM would be done at
+    const float units_all = (float)units_n * HG;
+    const float all = ((float)total * HG * kTile + units_all * (lane ? extra : kTile)) / slots;
+    float end = fmaxf(units_all > slots ? all + 0.5f * mine * kTile : all, (float)mine * kTile + extra);
+    if (cuts > p.cap) end = INFINITY;
+    float best = end;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) best = fminf(best, __shfl_xor_sync(kAll, best, off));
+    return __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, end == best)) - 1);
+}
+
 // The launch's work plan, the same in every CTA, by all its threads: len[s]
 // tiles of sequence s (0: no work), order[] the sequences with work, pre[i]
 // the parts of those before the i-th; vars: how many have work, how many of
@@ -223,7 +214,39 @@ __device__ void make_plan(const TreeParams &p, int32_t *pre, int32_t *len, uint1
         len[s] = r.n > 0 ? (r.ctx + kTile - 1) / kTile : 0;
     }
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 0 && S <= 32) {
+        // a sequence a lane: the plan below without its loops
+        const int l = lane < S ? len[lane] : 0;
+        const int total = __reduce_add_sync(kAll, l), longest = __reduce_max_sync(kAll, l);
+        const int some = __popc(__ballot_sync(kAll, l > 0));
+        const int mine = max(1, (longest + lane) / (lane + 1));
+        int units_n = 0, cuts = 0;
+        for (int s = 0; s < S; ++s) {
+            const int parts = (__shfl_sync(kAll, l, s) + mine - 1) / mine;
+            units_n += parts;
+            cuts += parts > 1 ? parts : 0;
+        }
+        const int P = part_size(p, total, longest, some, HG, mine, units_n, cuts, lane);
+        const int parts = (l + P - 1) / P, key = parts > 1 ? INT_MAX : l;
+        int rank = 0;
+        for (int s = 0; s < S; ++s) {
+            const int other = __shfl_sync(kAll, key, s);
+            rank += other > key || (other == key && s < lane);
+        }
+        if (l > 0) {
+            order[rank] = (uint16_t)lane;
+            counts[rank] = parts;
+        }
+        __syncwarp();
+        const int here = lane < some ? counts[lane] : 0, incl = warp_incl_scan(here, lane);
+        if (lane < some) pre[lane] = incl - here;
+        if (lane == max(some, 1) - 1) pre[some] = incl;
+        const int n_cut = __popc(__ballot_sync(kAll, parts > 1));
+        if (lane == 0) {
+            vars[0] = some;
+            vars[1] = n_cut;
+        }
+    } else if (warp == 0) {
         const int per = (S + 31) / 32, lo_s = min(S, lane * per), hi_s = min(S, lo_s + per);
         long long total = 0;
         int some = 0, longest = 0;
@@ -238,36 +261,15 @@ __device__ void make_plan(const TreeParams &p, int32_t *pre, int32_t *len, uint1
             some += __shfl_xor_sync(kAll, some, off);
             longest = max(longest, __shfl_xor_sync(kAll, longest, off));
         }
-        // How many tiles a part may have, P.  A unit costs its tiles, about one
-        // more to get going, and where it is a part of a cut sequence the
-        // writing and joining of its rows.
-        const int slots = gridDim.x, extra = kTile + 2 * p.max_q;     // in tokens
-        int P = longest, cut_parts;
-        if ((long long)some * HG < 4 * slots) {
-            // few units: the longest sequence in 1 to 32 parts, a lane each,
-            // by what the last SM would be done at
-            const int mine = (longest + lane) / (lane + 1);
-            long long units_n = 0;
-            int cuts = 0;
+        const int mine = max(1, (longest + lane) / (lane + 1));
+        int units_n = 0, cuts = 0, cut_parts;
+        if ((long long)some * HG < 4 * (int)gridDim.x)
             for (int s = 0; s < S; ++s) {
-                const int parts = mine ? (len[s] + mine - 1) / mine : 0;
-                units_n += parts;
-                cuts += parts > 1 ? parts : 0;
+                const int n = (len[s] + mine - 1) / mine;
+                units_n += n;
+                cuts += n > 1 ? n : 0;
             }
-            units_n *= HG;
-            const float all = ((float)total * HG * kTile + (float)(units_n * (lane ? extra : kTile))) / slots;
-            float end = fmaxf(units_n > slots ? all + 0.5f * mine * kTile : 0.f, (float)mine * kTile + extra);
-            end = fmaxf(end, all);
-            if (cuts > p.cap) end = INFINITY;
-            float best = end;
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) best = fminf(best, __shfl_xor_sync(kAll, best, off));
-            P = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, end == best)) - 1);
-        } else {
-            // many: parts of a quarter of an SM's share
-            P = (int)((total * HG + 4 * slots - 1) / (4 * slots));
-        }
-        P = max(P, 1);
+        int P = part_size(p, total, longest, some, HG, mine, units_n, cuts, lane);
         while (true) {   // (more than the cap only where the first case found none)
             cut_parts = 0;
             for (int s = lo_s; s < hi_s; ++s)
@@ -300,9 +302,9 @@ __device__ void make_plan(const TreeParams &p, int32_t *pre, int32_t *len, uint1
         __syncwarp();
         const int n_ord = start, per2 = (n_ord + 31) / 32;
         const int lo_i = min(n_ord, lane * per2), hi_i = min(n_ord, lo_i + per2);
-        int mine = 0;
-        for (int i = lo_i; i < hi_i; ++i) mine += (len[order[i]] + P - 1) / P;
-        int run = warp_incl_scan(mine, lane) - mine;
+        int parts = 0;
+        for (int i = lo_i; i < hi_i; ++i) parts += (len[order[i]] + P - 1) / P;
+        int run = warp_incl_scan(parts, lane) - parts;
         for (int i = lo_i; i < hi_i; ++i) {
             pre[i] = run;
             run += (len[order[i]] + P - 1) / P;
@@ -329,7 +331,6 @@ __device__ void make_plan(const TreeParams &p, int32_t *pre, int32_t *len, uint1
                 p.plan[order[i]] = make_int2(pre[i], pre[i + 1] - pre[i]);
         }
     }
-
 }
 
 // Which nodes see each node of a sequence (itself and its descendants): every
@@ -384,52 +385,62 @@ __device__ __forceinline__ void nodes_seen_by(const TreeParams &p, const SeqRows
 
 // ------------------------------------------------------------ main kernel
 
-constexpr int kSoftmaxWarps = 4, kProducer = 4, kProducts = 5, kQueries = 6, kThreads = 224;
 constexpr int kMinStages = 4, kMaxStages = 12;
 
 template <int D, int NQ>
 struct TreeCfg {
     static constexpr int NP = D / 64;                        // 64-column panels of a row
     static constexpr int HALF = kTile * D * 2;               // keys or values of a tile: a ring stage
+    // softmax warps: a token of the tile a thread, with more than 16 rows two
+    // threads a token, each half of the rows; then the warps that stream the
+    // ring, issue the products and fetch Q
+    static constexpr int SW = NQ == 16 ? 4 : 8, CQ = NQ / (SW / 4);
+    static constexpr int PRODUCER = SW, PRODUCTS = SW + 1, Q_WARP = SW + 2;
+    static constexpr int THREADS = (SW + 3) * 32;
     // tensor-memory columns: two S, O (a power of two in all)
     static constexpr uint32_t S_COL = 0, O_COL = 2 * NQ, COLS = 4 * NQ;
-    static constexpr int BARS = 0;                           // full, empty; units; q, s, p, o, done
-    static constexpr int VARS = BARS + (2 * kMaxStages + 2 * kUnitSlots + 2 + 2 + 2 + 1 + 1) * 8;
+    static constexpr int BARS = 0;                           // full, empty; units; q, s, p, seen, o, done
+    static constexpr int VARS = BARS + (2 * kMaxStages + 3 * kUnitSlots + 2 * 2 + 2 + 2 + 1 + 1) * 8;
     static constexpr int UNITS = (VARS + 16 + 15) / 16 * 16;
     static constexpr int SEEN = UNITS + kUnitSlots * 64;     // 64 x u64 per slot
-    static constexpr int RED = SEEN + kUnitSlots * 64 * 8;   // per warp and row
-    static constexpr int REF = RED + kSoftmaxWarps * NQ * 4; // reference maxima, corrections
+    static constexpr int RED = SEEN + kUnitSlots * 64 * 8;   // per 32 tokens and row
+    static constexpr int REF = RED + 4 * NQ * 4;             // reference maxima, corrections
     static constexpr int PLAN = REF + 2 * NQ * 4;            // pre[S+1], len[S], order[S]
     static constexpr int Q_BYTES = NQ * D * 2;               // [panel][row][128 bytes]
+    static constexpr int QB = Q_BYTES > 8192 ? 1 : 2;        // buffers of it
     static constexpr int P_BYTES = kTile * 128;              // [token][128 bytes], rows of 64 columns
     static int plan_bytes(int S) { return (S + 1) * 4 + S * 4 + (S + 1) / 2 * 4; }
     static int bytes(int S, int stages) {
-        return PLAN + plan_bytes(S) + 1024 + Q_BYTES + 2 * P_BYTES + stages * HALF;
+        return PLAN + plan_bytes(S) + 1024 + QB * Q_BYTES + 2 * P_BYTES + stages * HALF;
     }
 };
 
-// Eight fp32 from shared memory, 16-byte aligned.
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
-// One barrier of the softmax warps.
+// One barrier of the softmax warps (N threads).  (A warp comes to a barrier,
+// and to the loads and stores of tensor memory, with all its lanes together:
+// the instructions are undefined otherwise, and lanes that parted at a branch
+// before need not have met again by themselves.)
+template <int N>
 __device__ __forceinline__ void softmax_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxWarps * 32) : "memory");
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 // The same; whether v held in any (all) of their threads.
+template <int N>
 __device__ __forceinline__ bool softmax_any(bool v) {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v), "n"(kSoftmaxWarps * 32)
+        : "r"((uint32_t)v), "n"(N)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ bool softmax_all(bool v) { return !softmax_any(!v); }
+template <int N>
+__device__ __forceinline__ bool softmax_all(bool v) {
+    return !softmax_any<N>(!v);
+}
 
 // Combines N values over a warp's lanes: on return v[0 .. max(N / 32, 1)) are
 // the results for values first, first + 1, ... (every lane has a share).
@@ -455,17 +466,17 @@ __device__ __forceinline__ int warp_combine(float (&v)[N], int lane, Op op) {
 }
 
 template <int D, int NQ, bool SCORES>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
     tree_attention_kernel(const TreeParams p, const __grid_constant__ TreeMaps maps) {
     using Cfg = TreeCfg<D, NQ>;
     constexpr int NP = Cfg::NP, HALF = Cfg::HALF;
-    constexpr int G = SCORES ? 1 : NQ / 8;               // groups of 8 rows worked on
-    constexpr int R = SCORES ? 1 : NQ;                   // rows worked on
+    constexpr int QB = Cfg::QB, SW = Cfg::SW, CQ = Cfg::CQ, ST = SW * 32;
+    constexpr int R = SCORES ? 1 : CQ;                   // rows a softmax thread works on
     extern __shared__ __align__(16) uint8_t smem[];
     const uint32_t bar_full = smem_addr(smem + Cfg::BARS), bar_empty = bar_full + kMaxStages * 8;
     const uint32_t bar_unit = bar_empty + kMaxStages * 8, bar_unit_free = bar_unit + kUnitSlots * 8;
-    const uint32_t bar_q = bar_unit_free + kUnitSlots * 8, bar_q_free = bar_q + 8, bar_s = bar_q_free + 8,
-                   bar_p = bar_s + 16, bar_o = bar_p + 16, bar_done = bar_o + 8;
+    const uint32_t bar_q = bar_unit_free + kUnitSlots * 8, bar_q_free = bar_q + 16, bar_s = bar_q_free + 16,
+                   bar_p = bar_s + 16, bar_seen = bar_p + 16, bar_o = bar_seen + 8 * kUnitSlots, bar_done = bar_o + 8;
     int32_t *vars = reinterpret_cast<int32_t *>(smem + Cfg::VARS);    // [2]: tensor-memory address
     int32_t *units = reinterpret_cast<int32_t *>(smem + Cfg::UNITS);
     uint64_t *seen = reinterpret_cast<uint64_t *>(smem + Cfg::SEEN);
@@ -490,22 +501,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kUnitSlots; ++i) {
             mbar_init(bar_unit + 8 * i, 1);
-            mbar_init(bar_unit_free + 8 * i, kSoftmaxWarps + 2);
+            mbar_init(bar_unit_free + 8 * i, SW + 2);
         }
-        mbar_init(bar_q, 1);
-        mbar_init(bar_q_free, 1);
+        for (int i = 0; i < QB; ++i) {
+            mbar_init(bar_q + 8 * i, 1);
+            mbar_init(bar_q_free + 8 * i, 1);
+        }
         mbar_init(bar_s, 1);
         mbar_init(bar_s + 8, 1);
-        mbar_init(bar_p, kSoftmaxWarps);
-        mbar_init(bar_p + 8, kSoftmaxWarps);
+        mbar_init(bar_p, SW);
+        mbar_init(bar_p + 8, SW);
+        for (int i = 0; i < kUnitSlots; ++i) mbar_init(bar_seen + 8 * i, 1);
         mbar_init(bar_o, 1);
         mbar_init(bar_done, 1);
         fence_barrier_init();
     }
-    if (warp == kProducts) tc::alloc(smem_addr(&vars[2]), Cfg::COLS);
+    allow_next_launch();
+    if (warp == Cfg::PRODUCTS) tc::alloc(smem_addr(&vars[2]), Cfg::COLS);
     make_plan<SCORES>(p, pre, len, order, vars, reinterpret_cast<int32_t *>(tiles_at), H);
     // columns of P that no row writes have to hold finite numbers
-    for (int i = tid; i < 2 * Cfg::P_BYTES / 16; i += kThreads)
+    for (int i = tid; i < 2 * Cfg::P_BYTES / 16; i += Cfg::THREADS)
         reinterpret_cast<uint4 *>(tiles_at + stages * HALF)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     tc::fence_before();
@@ -515,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_ord = vars[0], n_units = pre[n_ord] * H;
     bool ok = true;
 
-    if (warp == kProducer) {
+    if (warp == Cfg::PRODUCER) {
         // ================================================ producer warp
         const uint64_t policy = l2_evict_first_policy();
         const uint32_t blk_bytes = (uint32_t)D * 2u << bshift;
@@ -583,9 +598,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 u[7] = cur.r.n;
                 u[8] = cur.r.row0;
             }
-            if (!last && (cur.b0 + cur.nb) << bshift > base)
-                nodes_seen_by<SCORES>(p, cur.r, lane, seen + slot * 64);
-            __syncwarp();
             if (lane == 0) mbar_arrive(bar_unit + 8 * slot);
             ++k_unit;
             if (last) break;
@@ -630,46 +642,60 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = max(0, issued - stages); k < issued; ++k)
                 mbar_wait_bounded(bar_full + 8 * (k % stages), (uint32_t)(k / stages) & 1u, p.status, false);
         }
-    } else if (warp == kQueries) {
-        // ================================================ queries, one thread
-        // (a warp of its own: the next unit's keys and values are on their way
-        // before this unit's last product has let go of Q)
-        if (lane == 0) {
-            uint32_t k = 0;
-            for (;; ++k) {
-                const int slot = k % kUnitSlots;
-                ok = mbar_wait_bounded(bar_unit + 8 * slot, (k / kUnitSlots) & 1u, p.status, true);
-                if (!ok) break;
-                const int32_t *u = units + slot * 16;
-                const int n_tok = u[5], h = u[1], row0 = u[8];
-                mbar_arrive(bar_unit_free + 8 * slot);
-                if (n_tok <= 0) break;
-                if (k > 0) ok = mbar_wait_bounded(bar_q_free, (k - 1) & 1u, p.status, true);
-                if (!ok) break;
-                mbar_arrive_expect_tx(bar_q, Cfg::Q_BYTES);
+    } else if (warp == Cfg::Q_WARP) {
+        // ================================================ queries
+        // Q of each unit, and which nodes see each node, by a warp of their own:
+        // the unit's keys and values need neither, and are on their way.
+        uint32_t k = 0;
+        for (;; ++k) {
+            const int slot = k % kUnitSlots, buf = k % QB;
+            ok = __all_sync(kAll, mbar_wait_bounded(bar_unit + 8 * slot, (k / kUnitSlots) & 1u, p.status, true));
+            if (!ok) break;
+            const int32_t *u = units + slot * 16;
+            const int n_tok = u[5], h = u[1];
+            const bool edge = u[4] + n_tok > u[6];           // the unit has nodes among its positions
+            const SeqRows r = {u[7], u[8], u[6] + u[7]};
+            if (n_tok <= 0) break;
+            if (k >= QB) ok = mbar_wait_bounded(bar_q_free + 8 * buf, (k / QB - 1) & 1u, p.status, true);
+            ok = __all_sync(kAll, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar_q + 8 * buf, Cfg::Q_BYTES);
 #pragma unroll
-                for (int pn = 0; pn < NP; ++pn) tma_load_3d(sQ + pn * NQ * 128, &maps.q, pn * 64, h, row0, bar_q);
+                for (int pn = 0; pn < NP; ++pn)
+                    tma_load_3d(sQ + buf * Cfg::Q_BYTES + pn * NQ * 128, &maps.q, pn * 64, h, r.row0,
+                                bar_q + 8 * buf);
             }
-            if (!ok) report(p.status, PA_ERR_TIMEOUT);
-            if (k > 0) mbar_wait_bounded(bar_q, (k - 1) & 1u, p.status, false);   // the last copy has landed
+            if (edge) nodes_seen_by<SCORES>(p, r, lane, seen + slot * 64);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar_seen + 8 * slot);
+                mbar_arrive(bar_unit_free + 8 * slot);
+            }
         }
+        if (!ok && lane == 0) report(p.status, PA_ERR_TIMEOUT);
+        // the last copies have landed
+        for (uint32_t i = k >= QB ? k - QB : 0; i < k; ++i)
+            mbar_wait_bounded(bar_q + 8 * (i % QB), (i / QB) & 1u, p.status, false);
         __syncwarp();
-    } else if (warp == kProducts) {
+    } else if (warp == Cfg::PRODUCTS) {
         // ================================================ products, one thread
         // Order: S of tile t + 1 before O of tile t, so that the softmax of a
         // tile finds its S ready; S and P have two buffers, taken in turn.
         if (lane == 0) {
             constexpr uint32_t idS = tc::idesc_f16(kTile, NQ, false);
             constexpr uint32_t idO = tc::idesc_f16(128, NQ, true) | (1u << 15);   // both MN-major
-            int st = 0, st_v = 0;        // stage of the next keys; of the current tile's values
+            int st = 0, st_v = 1;        // stage of the next keys; of the next values
             uint32_t use = 0, use_v = 0, gs = 0, gp = 0;   // tiles whose S, whose O was issued
+            uint32_t q_buf = 0;
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 ok = ok && mbar_wait_bounded(bar, parity, p.status, true);
                 return ok;
             };
             auto step = [&](int &i, uint32_t &n) {
-                if (++i == stages) {
-                    i = 0;
+                i += 2;
+                if (i >= stages) {
+                    i -= stages;
                     ++n;
                 }
             };
@@ -678,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(bar_full + 8 * st, use & 1u)) return;
                 tc::fence_after();
                 const uint64_t dk = tc::smem_desc(ring + st * HALF, 16, 1024u * NP);
-                const uint64_t dq = tc::smem_desc(sQ, 16, 1024);
+                const uint64_t dq = tc::smem_desc(sQ + q_buf * Cfg::Q_BYTES, 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     tc::mma_ss(tmem + Cfg::S_COL + (gs & 1) * NQ,
@@ -688,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::commit(bar_s + 8 * (gs & 1));
                 ++gs;
                 step(st, use);
-                step(st, use);
             };
             for (uint32_t k = 0;; ++k) {
                 const int slot = k % kUnitSlots;
@@ -696,14 +721,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n_tiles = (units[slot * 16 + 5] + kTile - 1) / kTile;
                 mbar_arrive(bar_unit_free + 8 * slot);
                 if (n_tiles == 0) break;
-                if (!wait(bar_q, k & 1u)) break;
+                q_buf = k % QB;
+                if (!wait(bar_q + 8 * q_buf, (k / QB) & 1u)) break;
                 issue_s();
-                if (n_tiles == 1) tc::commit(bar_q_free);
+                if (n_tiles == 1) tc::commit(bar_q_free + 8 * q_buf);
                 for (int t = 0; ok && t < n_tiles; ++t) {
-                    step(st_v, use_v);                   // past the keys
                     if (t + 1 < n_tiles) {
                         issue_s();
-                        if (t + 2 == n_tiles) tc::commit(bar_q_free);
+                        if (t + 2 == n_tiles) tc::commit(bar_q_free + 8 * q_buf);
                     }
                     if (!wait(bar_full + 8 * st_v, use_v & 1u) || !wait(bar_p + 8 * (gp & 1), (gp >> 1) & 1u)) break;
                     tc::fence_after();
@@ -727,149 +752,162 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // ================================================ softmax warps
-        // Thread = token of the tile (then, for O, dimension of the head).  The
-        // warps go through barriers together: a wait that fails only clears
-        // ok until the next vote.
-        const int tok = tid;
-        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        // Thread = token of the tile (then, for O, dimension of the head) and
+        // CQ of the rows.  The warps go through barriers together: a wait that
+        // fails only clears ok until the next vote.
+        const int tok = tid & 127, col0 = (warp >> 2) * CQ;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float qs = p.qscale;
         uint32_t g = 0;                                  // tiles so far
-        int st_v = 0;                                    // stage of the tile's values
+        int st_v = 1;                                    // stage of the tile's values
         uint32_t use_v = 0;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             ok = __all_sync(kAll, ok && mbar_wait_bounded(bar, parity, p.status, true));
         };
-        auto step = [&]() {
-            if (++st_v == stages) {
-                st_v = 0;
-                ++use_v;
-            }
-        };
-        // columns [c, c + N) of this thread's lane
-        auto load_cols = [&](uint32_t col, float (&v)[NQ]) {
-            uint32_t r[NQ];
-            if constexpr (NQ == 16) tc::ld16(lane_base + col, r);
-            else if constexpr (NQ == 32) tc::ld32(lane_base + col, r);
-            else tc::ld64(lane_base + col, r);
+        // CQ columns of this thread's lane
+        auto load_cols = [&](uint32_t col, float (&v)[CQ]) {
+            uint32_t r[CQ];
+            __syncwarp();
+            if constexpr (CQ == 16) tc::ld16(lane_base + col + col0, r);
+            else tc::ld32(lane_base + col + col0, r);
             tc::wait_ld();
 #pragma unroll
-            for (int i = 0; i < NQ; ++i) v[i] = __uint_as_float(r[i]);
+            for (int i = 0; i < CQ; ++i) v[i] = __uint_as_float(r[i]);
         };
         for (uint32_t k = 0;; ++k) {
             const int slot = k % kUnitSlots;
             wait(bar_unit + 8 * slot, (k / kUnitSlots) & 1u);
-            if (!softmax_all(ok)) break;
+            if (!softmax_all<ST>(ok)) break;
             const int32_t *u = units + slot * 16;
             const int s = u[0], h = u[1], part = u[2], parts = u[3], tok_first = u[4], n_tok = u[5], base = u[6],
                       n = u[7], row0 = u[8];
             if (n_tok <= 0) break;                       // the end
-            float l[R];
+            const int have = n - col0;                   // rows of this thread's that exist
+            bool knows = false;                          // who sees the nodes is there
+            float l[R], off[R];                          // running sums; minus the rows' references
 #pragma unroll
-            for (int i = 0; i < R; ++i) l[i] = 0.f;
+            for (int i = 0; i < R; ++i) l[i] = off[i] = 0.f;
             for (int t0 = 0; t0 < n_tok; t0 += kTile) {
                 const int nv = min(kTile, n_tok - t0);
-                step();                                  // past the keys' stage
-                wait(bar_s + 8 * (g & 1), (g >> 1) & 1u);
-                tc::fence_after();
-                float y[NQ];
-                load_cols(Cfg::S_COL + (g & 1) * NQ, y);
                 const int pos = tok_first + t0 + tok;
-#pragma unroll
-                for (int i = 0; i < R; ++i) y[i] *= qs;
-                if (tok_first + t0 + kTile > base || nv < kTile) {
-                    // who sees this position: every row before the nodes, then
-                    // the node itself and its descendants; none past the end
-                    const uint64_t v = tok >= nv ? 0ull : pos < base ? ~0ull : seen[slot * 64 + pos - base];
-#pragma unroll
-                    for (int i = 0; i < R; ++i)
-                        if (!((v >> i) & 1)) y[i] = -INFINITY;
+                const uint32_t b = g & 1;
+                wait(bar_s + 8 * b, (g >> 1) & 1u);
+                tc::fence_after();
+                if (tok_first + t0 + kTile > base && !knows) {
+                    wait(bar_seen + 8 * slot, (k / kUnitSlots) & 1u);
+                    knows = true;
                 }
-                if (SCORES && tok < nv) p.scores[((size_t)s * H + h) * p.score_stride + pos] = y[0];
+                // the tile's scores less the references, -inf where the row does not see
+                float y[CQ];
+                auto scores = [&]() {
+                    load_cols(Cfg::S_COL + b * NQ, y);
+                    if (SCORES && tok < nv)
+                        p.scores[((size_t)s * H + h) * p.score_stride + pos] = y[0] * qs;
+#pragma unroll
+                    for (int i = 0; i < R; ++i) y[i] = fmaf(y[i], qs, off[i]);
+                    if (tok_first + t0 + kTile > base || nv < kTile) {
+                        // who sees this position: every row before the nodes, then
+                        // the node itself and its descendants; none past the end
+                        const uint64_t v = (tok >= nv ? 0ull : pos < base ? ~0ull : seen[slot * 64 + pos - base]) >> col0;
+#pragma unroll
+                        for (int i = 0; i < R; ++i)
+                            if (!((v >> i) & 1)) y[i] = -INFINITY;
+                    }
+                };
+                scores();
                 // a row's reference moves when a score passes it by more than 2^8
                 bool over = t0 == 0;
                 if (t0 > 0) {
                     float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < G; ++c) {
-                        if (8 * c >= n) break;
-                        float f[8];
-                        load8(ref + 8 * c, f);
+                    for (int c = 0; c < R; c += 8)
+                        if (c < have) {
 #pragma unroll
-                        for (int e = 0; e < (SCORES ? 1 : 8); ++e) top = fmaxf(top, y[8 * c + e] - f[e]);
-                    }
+                            for (int i = c; i < c + 8 && i < R; ++i) top = fmaxf(top, y[i]);
+                        }
                     over = top > kRescaleLog2;
                 }
-                if (softmax_any(over || !ok)) {
-                    if (!softmax_all(ok)) break;
+                if (softmax_any<ST>(over || !ok)) {
+                    if (!softmax_all<ST>(ok)) break;
+                    if (t0 > 0) {                        // the scores themselves
+#pragma unroll
+                        for (int i = 0; i < R; ++i) off[i] = 0.f;
+                        scores();
+                    }
                     float m[R];
 #pragma unroll
                     for (int i = 0; i < R; ++i) m[i] = y[i];
-                    const int first = warp_combine(m, lane, [](float a, float b) { return fmaxf(a, b); });
+                    const int first = warp_combine(m, lane, [](float a, float c) { return fmaxf(a, c); });
 #pragma unroll
-                    for (int i = 0; i < (R + 31) / 32; ++i) red[warp * NQ + first + i] = m[i];
-                    softmax_sync();
-                    if (tid < R) {
-                        float top = red[tid];
-#pragma unroll
-                        for (int w = 1; w < kSoftmaxWarps; ++w) top = fmaxf(top, red[w * NQ + tid]);
+                    for (int i = 0; i < (R + 31) / 32; ++i) red[(warp & 3) * NQ + col0 + first + i] = m[i];
+                    softmax_sync<ST>();
+                    if (tid < (SCORES ? 1 : NQ)) {
+                        const float top = fmaxf(fmaxf(red[tid], red[NQ + tid]), fmaxf(red[2 * NQ + tid], red[3 * NQ + tid]));
                         // (a row that has seen nothing yet has reference -2^100: its
                         // terms, if any come, are rescaled from 0)
                         const float old = t0 ? ref[tid] : -0x1p100f, now = top > old + kRescaleLog2 ? top : old;
                         ref[tid] = now;
                         corr[tid] = ex2(old - now);
                     }
-                    softmax_sync();
+                    softmax_sync<ST>();
+#pragma unroll
+                    for (int i = 0; i < R; ++i) off[i] = -ref[col0 + i];
                     if (t0 > 0) {
 #pragma unroll
-                        for (int i = 0; i < R; ++i) l[i] *= corr[i];
-                        // O up to the tile before: its product gave the values' stage back
-                        const int ps = st_v >= 2 ? st_v - 2 : st_v - 2 + stages;
-                        wait(bar_empty + 8 * ps, (st_v >= 2 ? use_v : use_v - 1) & 1u);
+                        for (int i = 0; i < R; ++i) l[i] *= corr[col0 + i];
+                        // O, complete up to the tile before once that gave its
+                        // values' stage back
+                        const int st_o = st_v >= 2 ? st_v - 2 : st_v - 2 + stages;
+                        wait(bar_empty + 8 * st_o, (st_v >= 2 ? use_v : use_v - 1) & 1u);
                         tc::fence_after();
-                        float o[NQ];
+                        float o[CQ];
                         load_cols(Cfg::O_COL, o);
 #pragma unroll
-                        for (int i = 0; i < R; ++i) o[i] *= corr[i];
-                        uint32_t r[NQ];
+                        for (int i = 0; i < R; ++i) o[i] *= corr[col0 + i];
+                        uint32_t r[CQ];
 #pragma unroll
-                        for (int i = 0; i < NQ; ++i) r[i] = __float_as_uint(o[i]);
-                        if constexpr (NQ == 16) tc::st16(lane_base + Cfg::O_COL, r);
-                        else if constexpr (NQ == 32) tc::st32(lane_base + Cfg::O_COL, r);
-                        else tc::st64(lane_base + Cfg::O_COL, r);
+                        for (int i = 0; i < CQ; ++i) r[i] = __float_as_uint(o[i]);
+                        __syncwarp();
+                        if constexpr (CQ == 16) tc::st16(lane_base + Cfg::O_COL + col0, r);
+                        else tc::st32(lane_base + Cfg::O_COL + col0, r);
                         tc::wait_st();
                     }
+                    scores();
                 }
                 // P of the tile: this token's row, in the second operand's layout
-                const uint32_t prow = sP + (g & 1) * Cfg::P_BYTES + (uint32_t)tok * 128u;
+                uint32_t w[(R + 7) / 8 * 4];
+                if constexpr (SCORES) {
+                    const float p0 = ex2(y[0]);
+                    l[0] += p0;
+                    w[0] = pack_half2(p0, 0.f);
+                    w[1] = w[2] = w[3] = 0;
+                } else {
 #pragma unroll
-                for (int c = 0; c < G; ++c) {
-                    if (8 * c >= n) break;
-                    float f[8];
-                    load8(ref + 8 * c, f);
-                    uint32_t w[4] = {0, 0, 0, 0};
-                    if constexpr (SCORES) {
-                        const float p0 = ex2(y[0] - f[0]);
-                        l[0] += p0;
-                        w[0] = pack_half2(p0, 0.f);
-                    } else {
+                    for (int c = 0; c < R; c += 8)
+                        if (c < have) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int i = 8 * c + 2 * e;
-                            const float p0 = ex2(y[i] - f[2 * e]), p1 = ex2(y[i + 1] - f[2 * e + 1]);
-                            l[i] += p0;
-                            l[i + 1] += p1;
-                            w[e] = pack_half2(p0, p1);
+                            for (int i = c; i < c + 8; i += 2) {
+                                const float p0 = ex2(y[i]), p1 = ex2(y[i + 1]);
+                                l[i] += p0;
+                                l[i + 1] += p1;
+                                w[i / 2] = pack_half2(p0, p1);
+                            }
                         }
-                    }
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     prow + (uint32_t)((c ^ (tok & 7)) << 4)),
-                                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                 : "memory");
                 }
+                // (the product that read this buffer's last P is done: this tile's S
+                // was issued after it)
+                const uint32_t prow = sP + b * Cfg::P_BYTES + (uint32_t)tok * 128u;
+#pragma unroll
+                for (int c = 0; c < R; c += 8)
+                    if (c < have)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         prow + (uint32_t)((((col0 + c) >> 3) ^ (tok & 7)) << 4)),
+                                     "r"(w[c / 2]), "r"(w[c / 2 + 1]), "r"(w[c / 2 + 2]), "r"(w[c / 2 + 3])
+                                     : "memory");
                 if (nv < kTile) {
                     // values past the end meet P = 0 and have to be finite: zeros
                     wait(bar_full + 8 * st_v, use_v & 1u);
-                    if (tok >= nv) {
+                    if (tok >= nv && col0 == 0) {
                         const uint32_t row = ring + st_v * HALF + (uint32_t)(tok >> 3) * (NP * 1024u) +
                                              (uint32_t)(tok & 7) * 128u;
 #pragma unroll
@@ -883,42 +921,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_p + 8 * (g & 1));
+                if (lane == 0) mbar_arrive(bar_p + 8 * b);
                 ++g;
-                step();
+                st_v += 2;
+                if (st_v >= stages) {
+                    st_v -= stages;
+                    ++use_v;
+                }
             }
-            if (!softmax_all(ok)) break;
+            if (!softmax_all<ST>(ok)) break;
             if (lane == 0) mbar_arrive(bar_unit_free + 8 * slot);
             // sums over the tokens
-            const int first = warp_combine(l, lane, [](float a, float b) { return a + b; });
+            const int first = warp_combine(l, lane, [](float a, float c) { return a + c; });
 #pragma unroll
-            for (int i = 0; i < (R + 31) / 32; ++i) red[warp * NQ + first + i] = l[i];
-            softmax_sync();
+            for (int i = 0; i < (R + 31) / 32; ++i) red[(warp & 3) * NQ + col0 + first + i] = l[i];
+            softmax_sync<ST>();
             const size_t part_row = ((size_t)part * H + h) * NQ;
-            if (tid < R) {
-                float sum = red[tid];
-#pragma unroll
-                for (int w = 1; w < kSoftmaxWarps; ++w) sum += red[w * NQ + tid];
+            if (tid < (SCORES ? 1 : NQ)) {
+                const float sum = (red[tid] + red[NQ + tid]) + (red[2 * NQ + tid] + red[3 * NQ + tid]);
                 corr[tid] = 1.f / sum;
                 if (parts > 1 && tid < n) p.ws_ml[part_row + tid] = make_float2(ref[tid], sum);
                 if (SCORES && parts == 1) p.ml_one[(size_t)s * H + h] = make_float2(ref[0], sum);
             }
-            softmax_sync();
+            softmax_sync<ST>();
             wait(bar_o, k & 1u);
             tc::fence_after();
-            float o[NQ];
+            float o[CQ];
             load_cols(Cfg::O_COL, o);
             if (tok < D) {                               // thread = dimension
                 if (parts == 1) {
-                    __half *dst = p.out + ((size_t)row0 * H + h) * D + tok;
+                    __half *dst = p.out + ((size_t)(row0 + col0) * H + h) * D + tok;
 #pragma unroll
                     for (int i = 0; i < R; ++i)
-                        if (i < n) dst[(size_t)i * H * D] = __float2half(o[i] * corr[i]);
+                        if (i < have) dst[(size_t)i * H * D] = __float2half(o[i] * corr[col0 + i]);
                 } else {
-                    float *dst = p.ws_acc + part_row * D + tok;
+                    float *dst = p.ws_acc + (part_row + col0) * D + tok;
 #pragma unroll
                     for (int i = 0; i < R; ++i)
-                        if (i < n) dst[i * D] = o[i];
+                        if (i < have) dst[i * D] = o[i];
                 }
             }
             __syncwarp();
@@ -928,9 +968,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // ---- teardown: every product drained (bounded), then tensor memory freed
+    __syncwarp();
     tc::fence_before();
     __syncthreads();
-    if (warp == kProducts) {
+    if (warp == Cfg::PRODUCTS) {
         if (lane == 0 && !mbar_wait_bounded(bar_done, 0, p.status, false)) report(p.status, PA_ERR_TIMEOUT);
         __syncwarp();
         tc::fence_after();
@@ -946,6 +987,7 @@ template <int D>
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int NR) {
     constexpr int DL = D / 32;
     const int lane = threadIdx.x & 31, H = p.num_heads;
+    wait_for_launch_before();
     const long long items = (long long)p.header[1] * H * NR;
     const long long step = (long long)gridDim.x * 8;
     for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += step) {
@@ -988,6 +1030,7 @@ __global__ void __launch_bounds__(256)
     const int h = blockIdx.x, s = blockIdx.y, H = p.num_heads, tid = threadIdx.x, lane = tid & 31;
     const int ctx = p.ctx_lens[s];
     const int p0 = blockIdx.z * kWeightChunk;
+    wait_for_launch_before();
     if (ctx <= 0) {      // nothing cached: the output is 0
         if (p0 == 0 && tid < D) p.out[((size_t)s * H + h) * D + tid] = __float2half(0.f);
         return;
@@ -1161,6 +1204,21 @@ bool tree_geometry_ok(const pa_pool_desc *d, std::string *why) {
     return true;
 }
 
+// A launch that may begin while the kernel before it ends.
+template <typename... Args>
+cudaError_t launch_after(void (*kern)(Args...), dim3 grid, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <int D, int NQ, bool SCORES>
 int launch_tree(TreeParams p, const TreeMaps &maps, const char *who, cudaStream_t st) {
     using Cfg = TreeCfg<D, NQ>;
@@ -1182,7 +1240,7 @@ int launch_tree(TreeParams p, const TreeMaps &maps, const char *who, cudaStream_
                   "room beside the largest batch's plan");
     cudaError_t e = cudaMemsetAsync(p.header, 0, 8, st);
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: memset: %s", who, cudaGetErrorString(e));
-    kern<<<sm_count(), kThreads, Cfg::bytes(p.n_seqs, p.stages), st>>>(p, maps);
+    kern<<<sm_count(), Cfg::THREADS, Cfg::bytes(p.n_seqs, p.stages), st>>>(p, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return PA_OK;
@@ -1291,9 +1349,8 @@ int launch_tree_attention(void *out, const void *q, const void *k_cache, const v
     if (rc != PA_OK) return rc;
     const int NR = padded_rows(max_q_len);
     const int blocks = (int)std::min<int64_t>((int64_t)p.cap * d->num_heads * NR / 8 + 1, (int64_t)sm_count() * 4);
-    if (d->head_dim == 64) tree_join_kernel<64><<<blocks, 256, 0, st>>>(p, NR);
-    else tree_join_kernel<128><<<blocks, 256, 0, st>>>(p, NR);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(d->head_dim == 64 ? tree_join_kernel<64> : tree_join_kernel<128>, dim3(blocks),
+                                       st, p, NR);
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: join launch: %s", who, cudaGetErrorString(e));
     return PA_OK;
 }
@@ -1337,10 +1394,9 @@ int launch_decode_attention_weights(void *out, float *weights_out, const float *
     const int rc = launch_common(who, true, p, k_cache, v_cache, workspace, workspace_bytes, 1, d, st);
     if (rc != PA_OK) return rc;
     const bool vec = weight_len % 4 == 0 && !mis(weights_out, 16) && !mis(weights_in, 16);
-    auto go = [&](auto kern) { kern<<<grid, 256, 0, st>>>(p, padded_rows(1), weights_out, weights_in); };
-    if (d->head_dim == 64) vec ? go(decode_weights_kernel<64, true>) : go(decode_weights_kernel<64, false>);
-    else vec ? go(decode_weights_kernel<128, true>) : go(decode_weights_kernel<128, false>);
-    const cudaError_t e = cudaGetLastError();
+    const auto kern = d->head_dim == 64 ? (vec ? decode_weights_kernel<64, true> : decode_weights_kernel<64, false>)
+                                        : (vec ? decode_weights_kernel<128, true> : decode_weights_kernel<128, false>);
+    const cudaError_t e = launch_after(kern, grid, st, p, padded_rows(1), weights_out, weights_in);
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: weights launch: %s", who, cudaGetErrorString(e));
     return PA_OK;
 }
