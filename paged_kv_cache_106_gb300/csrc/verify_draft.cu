@@ -16,26 +16,29 @@
 //
 // Exactness.  A running sum crosses an edge at every token, so rounding of
 // 2^-24 in it would move the answer once in some hundred samples at 50 k
-// tokens.  All weights are therefore pairs of fp32 (value + error term, 2^-48),
-// added with error-free transformations; only the joining of the warps' sums
-// and the tests of single tokens are in fp64, in one warp (this GPU does two
-// fp64 operations a clock and SM: with sums joined in fp64 by every thread
-// 256 rows of 50 k tokens took 342 us, this way ...).  No atomics: the result depends
-// only on the inputs.
+// tokens.  All weights and sums are therefore pairs of fp32 (value + error
+// term, 2^-46 or better in all), added with error-free transformations; in
+// fp64 the additions alone would take three times a row's bytes (this GPU does
+// two fp64 operations a clock and SM).  No atomics: the result depends only on
+// the inputs.
 //
 // What bounds it: the rows it has to read (one target row, and one draft row
 // once something is rejected, 4 V bytes each) for a large batch; the chain of
-// dependent loads for a small one.  Per sequence one cluster of up to 8 CTAs
-// shares a row: first the scalars p_parent(x), q_parent(x), u of all nodes are
-// gathered at once, so the walk itself touches no memory (a chain never needs
-// a pass over a row before the last one), then each pass over a row is split
-// evenly over the cluster's warps, contiguous spans in order of index, and the
-// warps' sums are exchanged through distributed shared memory.
+// dependent loads and barriers for a small one.  Per sequence one cluster of
+// up to 8 CTAs shares a row: first the scalars p_parent(x), q_parent(x), u of
+// all nodes are gathered at once, so the walk itself touches no memory (a
+// chain never needs a pass over a row before the last one), then each pass over
+// a row is split evenly over the cluster's warps, contiguous spans in order of
+// index, whose sums go to every CTA of the cluster.  A warp knows the sums of
+// its rows of 128 tokens, so the one in whose span the target falls scans
+// one of them.  The code is kept short: a CTA goes through it about once, and
+// with everything unrolled its instructions came slower than the data.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -45,9 +48,11 @@ namespace pagedkv {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = 8, kThreads = kWarps * 32, kPerSm = 4;
 constexpr int kMaxCluster = 8;
-static_assert(kMaxCluster * kWarps <= 64, "a lane of warp 0 takes two warps' sums");
+constexpr int kPerLane = kMaxCluster * kWarps / 32;   // warps' sums a lane of warp 0 takes
+constexpr int kRound = 4;                             // rows of 128 tokens a warp loads at a time
+constexpr int kSegments = 32;                         // sums a warp keeps of its span
 constexpr int kNodes = PA_TREE_MAX_NODES;
 
 struct VerifyParams {
@@ -55,7 +60,8 @@ struct VerifyParams {
     const void *p, *q;
     const int32_t *tokens, *parents, *q_starts;
     const float *u_accept, *u_sample;
-    int32_t max_q, q_rows, vocab, span;   // span: elements a warp owns
+    int32_t max_q, q_rows, vocab;
+    int32_t rows, segment;   // rows of 128 a warp owns, and of one of its segments (a multiple of kRound)
     int32_t *status;
 };
 
@@ -81,6 +87,26 @@ __device__ __forceinline__ bool above(Pair a, Pair b) {
     return __fadd_rn(d.hi, __fadd_rn(d.lo, __fsub_rn(a.lo, b.lo))) > 0.f;
 }
 
+// The running sum a and one weight more; a.lo collects the errors.
+__device__ __forceinline__ Pair plus(Pair a, Pair w) {
+    const Pair t = two_sum(a.hi, w.hi);
+    return {t.hi, __fadd_rn(a.lo, __fadd_rn(t.lo, w.lo))};
+}
+
+// max(p - q, 0), exact: what is left where p > q has p as the larger term.
+__device__ __forceinline__ Pair less(float p, float q) {
+    const float d = __fsub_rn(p, q), e = __fsub_rn(__fsub_rn(p, d), q);
+    return d > 0.f ? Pair{d, e} : Pair{0.f, 0.f};
+}
+
+// a b z
+__device__ __forceinline__ Pair times(float a, float b, Pair z) {
+    const float p = __fmul_rn(a, b), e = __fmaf_rn(a, b, -p);
+    const float h = __fmul_rn(p, z.hi);
+    const float l = __fadd_rn(__fmaf_rn(p, z.hi, -h), __fmaf_rn(p, z.lo, __fmul_rn(e, z.hi)));
+    return {h, l};
+}
+
 // max(w - z q, 0), z = zh + zl
 __device__ __forceinline__ Pair reject(Pair w, float q, float zh, float zl) {
     const float ph = __fmul_rn(q, zh);
@@ -95,33 +121,45 @@ __device__ __forceinline__ Pair reject(Pair w, float q, float zh, float zl) {
 }
 
 // Probabilities that are not positive and finite count as 0.
-__device__ __forceinline__ float clean(float x) { return x > 0.f && x <= FLT_MAX ? x : 0.f; }
+__device__ __forceinline__ float clean(float x) {
+    return __float_as_uint(x) < 0x7f800000u ? x : 0.f;   // (negative: the top bit; NaN: above infinity)
+}
 
 __device__ __forceinline__ float value(const float *p) { return clean(__ldg(p)); }
 __device__ __forceinline__ float value(const __half *p) { return clean(__half2float(__ldg(p))); }
 __device__ __forceinline__ float value(const __nv_bfloat16 *p) { return clean(__bfloat162float(__ldg(p))); }
 
-// VEC consecutive values (one load when VEC > 1).
-template <typename T, int VEC>
-__device__ __forceinline__ void values(const T *p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = value(p);
-    } else if constexpr (sizeof(T) == 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
-        v[0] = clean(x.x);
-        v[1] = clean(x.y);
-        v[2] = clean(x.z);
-        v[3] = clean(x.w);
-    } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
-        T h[4];
-        *reinterpret_cast<uint2 *>(h) = x;
+// Elements x .. x + 3 of a row of V, 0 outside it, one by one.
+template <typename T>
+__device__ __noinline__ float4 edge4(const T *row, int x, int V) {
+    float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (std::is_same<T, __half>::value) v[i] = clean(__half2float(h[i]));
-            else v[i] = clean(__bfloat162float(h[i]));
-        }
+    for (int i = 0; i < 4; ++i) v[i] = x + i >= 0 && x + i < V ? value(row + x + i) : 0.f;
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+// Four elements as they lie in memory.
+template <typename T>
+struct Raw {
+    using type = uint2;
+};
+template <>
+struct Raw<float> {
+    using type = uint4;
+};
+__device__ __forceinline__ float4 unpack(const uint4 &r, float) {
+    return make_float4(clean(__uint_as_float(r.x)), clean(__uint_as_float(r.y)), clean(__uint_as_float(r.z)),
+                       clean(__uint_as_float(r.w)));
+}
+template <typename T>
+__device__ __forceinline__ float4 unpack(const uint2 &r, T) {
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint16_t b = (uint16_t)((i < 2 ? r.x : r.y) >> (16 * (i & 1)));
+        if constexpr (std::is_same<T, __half>::value) v[i] = clean(__half2float(__ushort_as_half(b)));
+        else v[i] = clean(__bfloat162float(__ushort_as_bfloat16(b)));
     }
+    return make_float4(v[0], v[1], v[2], v[3]);
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -137,12 +175,10 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ double load_cluster(const Pair *local, uint32_t rank) {
+__device__ __forceinline__ void store_cluster(Pair *local, uint32_t rank, Pair v) {
     uint32_t a;
-    Pair v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.hi), "=f"(v.lo) : "r"(a) : "memory");
-    return (double)v.hi + (double)v.lo;
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.hi), "f"(v.lo) : "memory");
 }
 
 struct Shared {
@@ -150,15 +186,16 @@ struct Shared {
     int32_t up[kNodes], tok[kNodes];
     float zh[kNodes], zl[kNodes];              // Z before each rejection at the current node
     int32_t out[kNodes];                       // the tokens rejected there
-    Pair wsum[2][kWarps];                      // this CTA's warps' sums, by parity of the pass
+    Pair sums[2][kMaxCluster * kWarps];        // the row's sums by warp, in order; by parity of the pass
+    Pair seg[kWarps][kSegments];               // of this CTA's warps' segments
     int32_t cur, k;                            // the row to add up: its node, rejections there
     int32_t owner;                             // the warp that finds the next token, or:
     Pair left;                                 // of the target, within the owner's span
 };
 enum { kAgain = -1, kNone = -2 };
 
-template <typename T, bool DRAFT, int VEC>
-__global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyParams a) {
+template <typename T, bool DRAFT, bool VEC>
+__global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const VerifyParams a) {
     __shared__ Shared sh;
     const uint32_t rank = cluster_rank(), C = cluster_size();
     const int s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -208,42 +245,93 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyPara
     }
     __syncthreads();
 
+    // Spans are counted from the vector boundary at or before the row's start.
     const int gw = (int)rank * kWarps + warp;          // this warp's place in the row
-    const int lo = (int)min((long long)V, (long long)gw * a.span);
-    const int hi = (int)min((long long)V, (long long)lo + a.span);
+    const int lo = gw * a.rows * 128 + lane * 4;       // this lane's first tokens of it
 
-    // The weights of VEC tokens from i on, after k rejections at node v.
-    auto weights = [&](int v, int k, int i, Pair (&w)[VEC]) {
-        float pv[VEC];
-        values<T, VEC>(P + (size_t)v * V + i, pv);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = {pv[e], 0.f};
-        if (k > 0) {
+    struct Row {
+        const T *p, *q;
+        int shift, k;                                  // elements before the row; rejections
+    };
+    auto row_of = [&](int v, int k) {
+        const long long at = (long long)v * V;
+        return Row{P + at, DRAFT ? Q + at : nullptr, VEC ? (int)(((long long)row0 * V + at) & 3) : 0, k};
+    };
+    // This lane's four weights of a 128, from their probabilities; x: the first's token.
+    auto weights = [&](const Row &r, int x, const float4 &pv, const float4 &qv, Pair (&w)[4]) {
+        w[0] = {pv.x, 0.f};
+        w[1] = {pv.y, 0.f};
+        w[2] = {pv.z, 0.f};
+        w[3] = {pv.w, 0.f};
+        if (DRAFT && r.k > 0) {          // (Z is 1 for the first rejection)
+            w[0] = less(pv.x, qv.x);
+            w[1] = less(pv.y, qv.y);
+            w[2] = less(pv.z, qv.z);
+            w[3] = less(pv.w, qv.w);
+        }
+#pragma unroll 1
+        for (int i = DRAFT ? 1 : 0; i < r.k; ++i) {
             if (DRAFT) {
-                float qv[VEC];
-                values<T, VEC>(Q + (size_t)v * V + i, qv);
-                for (int r = 0; r < k; ++r) {
-                    const float zh = sh.zh[r], zl = sh.zl[r];
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) w[e] = reject(w[e], qv[e], zh, zl);
-                }
+                const float zh = sh.zh[i], zl = sh.zl[i];
+                w[0] = reject(w[0], qv.x, zh, zl);
+                w[1] = reject(w[1], qv.y, zh, zl);
+                w[2] = reject(w[2], qv.z, zh, zl);
+                w[3] = reject(w[3], qv.w, zh, zl);
             } else {
-                for (int r = 0; r < k; ++r) {
-                    const int x = sh.out[r] - i;
+                const int out = sh.out[i] - x;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (x == e) w[e] = {0.f, 0.f};
-                }
+                for (int e = 0; e < 4; ++e)
+                    if (out == e) w[e] = {0.f, 0.f};
             }
         }
     };
+    // This lane's sums of kRound rows of 128 from row j on.
+    auto round_sums = [&](const Row &r, int j, Pair (&t)[kRound]) {
+        // every load first, each on its own: nothing between them waits for one
+        typename Raw<T>::type pr[kRound] = {}, qr[kRound] = {};
+#pragma unroll
+        for (int b = 0; b < kRound; ++b) {
+            const int x = lo + (j + b) * 128 - r.shift;
+            if (VEC && j + b < a.rows && x >= 0 && x + 4 <= V) {
+                pr[b] = __ldg(reinterpret_cast<const typename Raw<T>::type *>(r.p + x));
+                if (DRAFT && r.k > 0) qr[b] = __ldg(reinterpret_cast<const typename Raw<T>::type *>(r.q + x));
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kRound; ++b) {
+            const int x = lo + (j + b) * 128 - r.shift;
+            float4 pv = unpack(pr[b], T()), qv = unpack(qr[b], T());
+            if (j + b < a.rows && (!VEC || x < 0 || x + 4 > V) && x < V) {   // a row's ends
+                pv = edge4(r.p, x, V);
+                if (DRAFT && r.k > 0) qv = edge4(r.q, x, V);
+            }
+            Pair w[4];
+            weights(r, x, pv, qv, w);
+            t[b] = plus(plus(plus(w[0], w[1]), w[2]), w[3]);
+        }
+    };
+    auto over_lanes = [&](Pair v) {
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            v = add(v, {__shfl_xor_sync(kAll, v.hi, off), __shfl_xor_sync(kAll, v.lo, off)});
+        return v;
+    };
+    // Running sums over a warp's lanes.
+    auto scan = [&](Pair incl) {
+#pragma unroll 1
+        for (int off = 1; off < 32; off <<= 1) {
+            const Pair y = {__shfl_up_sync(kAll, incl.hi, off), __shfl_up_sync(kAll, incl.lo, off)};
+            if (lane >= off) incl = add(incl, y);
+        }
+        return incl;
+    };
+    auto from_lane = [&](const Pair &v, int l) { return Pair{__shfl_sync(kAll, v.hi, l), __shfl_sync(kAll, v.lo, l)}; };
 
-    // Warp 0 of every CTA walks (alike, in fp64: a few operations a node; the
-    // other warps would only queue for the fp64 unit) up to where the sum of a
-    // row is needed, all warps add up that row, warp 0 goes on.
+    // Warp 0 of every CTA walks (alike) up to where the sum of a row is needed,
+    // all warps add up that row, warp 0 goes on.
     int i = 1, cur = 0, k = 0, len = 1;
     bool pending = false;       // the last rejection's sum is not known yet
-    double z = 1.;
+    Pair z = {1.f, 0.f};
     int32_t *path = a.path + (size_t)s * a.max_q;
     const bool writer = rank == 0 && tid == 0;
     if (writer) path[0] = 0;
@@ -260,18 +348,17 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyPara
                     for (int r = 0; r < k; ++r)
                         if (sh.out[r] == sh.tok[i]) w = {0.f, 0.f};
                 }
-                // (u q is exact in fp64)
-                if ((double)sh.u[i] * (double)qx * z < (double)w.hi + (double)w.lo) {
+                if (above(w, times(sh.u[i], qx, z))) {
                     cur = i;
                     k = 0;
-                    z = 1.;
+                    z = {1.f, 0.f};
                     if (writer) path[len] = i;
                     ++len;
                 } else {
                     __syncwarp();       // every lane has read the list's earlier entries
                     if (lane == 0) {
-                        sh.zh[k] = (float)z;
-                        sh.zl[k] = (float)(z - (double)(float)z);
+                        sh.zh[k] = z.hi;
+                        sh.zl[k] = z.lo;
                         sh.out[k] = sh.tok[i];
                     }
                     __syncwarp();
@@ -285,61 +372,68 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyPara
             }
         }
         __syncthreads();
-        const int v = sh.cur, kk = sh.k;
+        const Row row = row_of(sh.cur, sh.k);
         Pair acc = {0.f, 0.f};
-#pragma unroll 4
-        for (int x = lo + lane * VEC; x < hi; x += 32 * VEC) {
-            Pair w[VEC];
-            weights(v, kk, x, w);
+#pragma unroll 1
+        for (int j = 0, g = 0; j < a.rows; ++g) {
+            Pair sum = {0.f, 0.f};
+#pragma unroll 1
+            for (const int end = j + a.segment; j < end; j += kRound) {
+                Pair t[kRound];
+                round_sums(row, j, t);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const Pair t = two_sum(acc.hi, w[e].hi);
-                acc = {t.hi, __fadd_rn(acc.lo, __fadd_rn(t.lo, w[e].lo))};
+                for (int b = 0; b < kRound; ++b) sum = plus(sum, t[b]);
             }
+            sum = over_lanes(sum);
+            if (lane == 0) sh.seg[warp][g] = sum;
+            acc = add(acc, sum);
         }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1)
-            acc = add(acc, {__shfl_xor_sync(kAll, acc.hi, off), __shfl_xor_sync(kAll, acc.lo, off)});
-        if (lane == 0) sh.wsum[parity][warp] = acc;
+        // to every CTA; two buffers, since a CTA of the cluster may still read the
+        // last pass's (none can be two passes behind)
+        if (lane < (int)C) store_cluster(&sh.sums[parity][gw], (uint32_t)lane, acc);
         cluster_sync();
         if (warp == 0) {
-            // lane l: the sums of warps 2l and 2l + 1 of the row
-            double w0 = 0., w1 = 0.;
-            const int g0 = 2 * lane, g1 = g0 + 1, all = (int)C * kWarps;
-            if (g0 < all) w0 = load_cluster(&sh.wsum[parity][g0 % kWarps], (uint32_t)(g0 / kWarps));
-            if (g1 < all) w1 = load_cluster(&sh.wsum[parity][g1 % kWarps], (uint32_t)(g1 / kWarps));
-            double incl = w0 + w1;
+            // lane l: the sums of warps kPerLane l .. of the row
+            const Pair zero = {0.f, 0.f};
+            Pair run[kPerLane];
+            int positive = -1;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const double y = __shfl_up_sync(kAll, incl, off);
-                if (lane >= off) incl += y;
+            for (int e = 0; e < kPerLane; ++e) {
+                const int w = kPerLane * lane + e;
+                const Pair v = w < (int)C * kWarps ? sh.sums[parity][w] : zero;
+                if (v.hi > 0.f) positive = w;
+                run[e] = e ? add(run[e - 1], v) : v;
             }
-            const double total = __shfl_sync(kAll, incl, 31);
+            const Pair incl = scan(run[kPerLane - 1]), total = from_lane(incl, 31);
             int owner = kAgain;
-            if (pending && !(total > 0.)) {      // nothing would be left: the weights stay
+            if (pending && !(total.hi > 0.f)) {  // nothing would be left: the weights stay
                 --k;
                 pending = false;
             } else if (i < n) {                  // on with the next child
                 if (pending) z = total;
                 pending = false;
-            } else if (!(total > 0.)) {
+            } else if (!(total.hi > 0.f)) {
                 owner = kNone;
                 if (writer) report(a.status, PA_ERR_INVALID_ARG);
             } else {
-                // the warp whose span the target falls into finds the token
-                const double target = (double)us * total, before = incl - (w0 + w1);
-                const unsigned m0 = __ballot_sync(kAll, before + w0 > target);
-                const unsigned m1 = __ballot_sync(kAll, incl > target);
-                const unsigned p0 = __ballot_sync(kAll, w0 > 0.), p1 = __ballot_sync(kAll, w1 > 0.);
-                const int f0 = m0 ? 2 * (__ffs(m0) - 1) : INT_MAX, f1 = m1 ? 2 * (__ffs(m1) - 1) + 1 : INT_MAX;
-                owner = min(f0, f1);
-                const bool past = owner == INT_MAX;   // the target rounds to the total or more
-                if (past)
-                    owner = max(p0 ? 2 * (31 - __clz(p0)) : 0, p1 ? 2 * (31 - __clz(p1)) + 1 : 0);
-                if (lane == owner / 2) {
-                    const double left = past ? INFINITY : target - (owner & 1 ? before + w0 : before);
-                    sh.left = {(float)left, past ? 0.f : (float)(left - (double)(float)left)};
+                // the warp whose span the target falls into finds the token; the
+                // last one with any weight where the target rounds to the total
+                const Pair target = times(us, 1.f, total);
+                Pair before = {__shfl_up_sync(kAll, incl.hi, 1), __shfl_up_sync(kAll, incl.lo, 1)}, from = zero;
+                if (lane == 0) before = zero;
+                int mine = INT_MAX;
+#pragma unroll
+                for (int e = kPerLane - 1; e >= 0; --e) {
+                    if (above(add(before, run[e]), target)) {
+                        mine = kPerLane * lane + e;
+                        from = e ? add(before, run[e > 0 ? e - 1 : 0]) : before;
+                    }
                 }
+                owner = __reduce_min_sync(kAll, mine);
+                const bool past = owner == INT_MAX;
+                if (past) owner = __reduce_max_sync(kAll, positive);
+                if (lane == owner / kPerLane)
+                    sh.left = past ? Pair{INFINITY, 0.f} : add(target, {-from.hi, -from.lo});
             }
             if (lane == 0) sh.owner = owner;
         }
@@ -353,48 +447,63 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(const VerifyPara
         if (rank == 0 && warp == 0)
             for (int x = len + lane; x < a.max_q; x += 32) path[x] = -1;
         if (gw == sh.owner) {
-            // the first token at which the span's running sum passes what is left
-            const Pair left = sh.left;
-            int found = INT_MAX, positive = -1;
-            Pair base = {0.f, 0.f};
-            for (int x0 = lo; x0 < hi && found == INT_MAX; x0 += 32 * VEC) {
-                const int x = x0 + lane * VEC;
-                Pair w[VEC], run[VEC];
+            // The first token at which the span's running sum passes what is
+            // left: its segment, its 128, itself.  (Rounding can leave the last
+            // ones short: then the last one of positive weight.)
+            const Pair left = sh.left, zero = {0.f, 0.f};
+            __syncwarp();
+            const Pair seg = lane * a.segment < a.rows ? sh.seg[warp][lane] : zero, upto = scan(seg);
+            unsigned m = __ballot_sync(kAll, seg.hi > 0.f && above(upto, left));
+            if (!m) m = 1u << (31 - __clz(__ballot_sync(kAll, seg.hi > 0.f) | 1u));
+            const int g = __ffs(m) - 1;
+            Pair before = g ? from_lane(upto, g - 1) : zero;
+            int in = -1;
+            Pair base = before;
+#pragma unroll 1
+            for (int j = g * a.segment; j < (g + 1) * a.segment; j += kRound) {
+                Pair t[kRound];
+                round_sums(row, j, t);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) w[e] = {0.f, 0.f};
-                if (x < hi) weights(v, kk, x, w);
+                for (int b = 0; b < kRound; ++b) t[b] = over_lanes(t[b]);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    run[e] = e ? add(run[e - 1], w[e]) : w[e];
-                    if (w[e].hi > 0.f) positive = x + e;
+                for (int b = 0; b < kRound; ++b) {
+                    if (t[b].hi > 0.f && !above(base, left)) {
+                        in = j + b;
+                        before = base;
+                    }
+                    base = add(base, t[b]);
                 }
-                Pair incl = run[VEC - 1];
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const Pair y = {__shfl_up_sync(kAll, incl.hi, off), __shfl_up_sync(kAll, incl.lo, off)};
-                    if (lane >= off) incl = add(incl, y);
-                }
-                Pair excl = {__shfl_up_sync(kAll, incl.hi, 1), __shfl_up_sync(kAll, incl.lo, 1)};
-                excl = lane == 0 ? base : add(base, excl);
-#pragma unroll
-                for (int e = VEC - 1; e >= 0; --e)
-                    if (w[e].hi > 0.f && above(add(excl, run[e]), left)) found = x + e;
-                base = add(base, {__shfl_sync(kAll, incl.hi, 31), __shfl_sync(kAll, incl.lo, 31)});
-                found = __reduce_min_sync(kAll, found);
             }
-            positive = __reduce_max_sync(kAll, positive);
-            // (rounding can leave the last element short of the warp's sum)
-            if (lane == 0) a.next_tokens[s] = found != INT_MAX ? found : positive;
+            const int x = lo + max(in, 0) * 128 - row.shift;
+            float4 qv = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 pv = edge4(row.p, x, V);
+            if (DRAFT && row.k > 0) qv = edge4(row.q, x, V);
+            Pair w[4];
+            weights(row, x, pv, qv, w);
+            int found = INT_MAX, last = -1;
+            const Pair incl = scan(add(add(w[0], w[1]), add(w[2], w[3])));
+            Pair run = {__shfl_up_sync(kAll, incl.hi, 1), __shfl_up_sync(kAll, incl.lo, 1)};
+            run = lane == 0 ? before : add(before, run);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                run = add(run, w[e]);
+                if (w[e].hi > 0.f) {
+                    last = x + e;
+                    if (found == INT_MAX && above(run, left)) found = x + e;
+                }
+            }
+            found = __reduce_min_sync(kAll, found);
+            last = __reduce_max_sync(kAll, last);
+            if (lane == 0) a.next_tokens[s] = found != INT_MAX ? found : last;
         }
-        break;
+        return;
     }
-    cluster_sync();   // no CTA leaves while another may read its sums
 }
 
 template <typename T, bool DRAFT>
 cudaError_t launch_vec(const VerifyParams &a, bool vec, const cudaLaunchConfig_t &cfg) {
-    return vec ? cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, DRAFT, 4>, a)
-               : cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, DRAFT, 1>, a);
+    return vec ? cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, DRAFT, true>, a)
+               : cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, DRAFT, false>, a);
 }
 template <typename T>
 cudaError_t launch_type(const VerifyParams &a, bool vec, const cudaLaunchConfig_t &cfg) {
@@ -424,12 +533,13 @@ int launch_verify_draft(int32_t *path, int32_t *path_lens, int32_t *next_tokens,
         mis(next_tokens, 4) || mis(draft_tokens, 4) || mis(parents, 4) || mis(q_starts, 4) ||
         mis(u_accept, 4) || mis(u_sample, 4) || mis(status, 4))
         return fail(PA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
-    // every row starts on a vector boundary
-    const bool vec = vocab % 4 == 0 && !mis(target_probs, 4 * size) && !mis(draft_probs, 4 * size);
-    const int step = vec ? 128 : 32;
-    // a CTA for every 2048 tokens, up to a cluster of 8
-    int C = 1;
-    while (C < kMaxCluster && (int64_t)C * 2048 < vocab) C *= 2;
+    const bool vec = !mis(target_probs, 4 * size) && !mis(draft_probs, 4 * size);
+    // Clusters of up to 8 CTAs, each CTA with 2048 tokens or more, and no more
+    // CTAs than the GPU holds at once: a sequence's fixed part (loads that wait
+    // on one another, barriers) is as long as its share of a row then.
+    int sms = 152, dev = 0, C = 1;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    while (C < kMaxCluster && (int64_t)C * 2048 < vocab && (int64_t)n_seqs * C * 2 <= (int64_t)sms * kPerSm) C *= 2;
     VerifyParams a{};
     a.path = path;
     a.path_lens = path_lens;
@@ -445,9 +555,9 @@ int launch_verify_draft(int32_t *path, int32_t *path_lens, int32_t *next_tokens,
     a.q_rows = q_rows;
     a.vocab = vocab;
     const int64_t warps = (int64_t)C * kWarps;
-    const int64_t span = ((vocab + warps - 1) / warps + step - 1) / step * step;
-    if (span > INT32_MAX / 2) return fail(PA_ERR_INVALID_ARG, "%s: vocab=%d too large", who, vocab);
-    a.span = (int32_t)span;
+    if (vocab > INT32_MAX / 2) return fail(PA_ERR_INVALID_ARG, "%s: vocab=%d too large", who, vocab);
+    a.rows = (int32_t)((((int64_t)vocab + 3 + warps - 1) / warps + 127) / 128);   // (3: up to a row's vector boundary)
+    a.segment = ((a.rows + kSegments - 1) / kSegments + kRound - 1) / kRound * kRound;
     a.status = status;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)C, (unsigned)n_seqs, 1);
