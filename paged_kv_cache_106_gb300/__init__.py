@@ -204,12 +204,10 @@ class PoolDesc:
                               None if self._free is None else
                               self._free.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)))
 
+        self.ref = ctypes.byref(self.c)
+
     def __getattr__(self, name):
         return getattr(self.__dict__["c"], name)
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.c)
 
 
 # ---------------------------------------------------------------- host calls
@@ -559,11 +557,38 @@ def pa_prefill_step_attention(out, q, k_new, v_new, k_cache, v_cache, block_tabl
                                           _stream(stream)))
 
 
-def _need_dtype(kind: str, **tensors):
-    """Refuses a tensor whose element type is not the one the call reads."""
-    for name, t in tensors.items():
-        if t is not None and not isinstance(t, int) and str(t.dtype) != "torch." + kind:
-            raise ValueError(f"{name} is {t.dtype}, the call reads {kind}")
+# The calls below take microseconds on the GPU, so their arguments are checked
+# with as few Python operations as will do.
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _arg(name, t, dtype, n):
+    """Device address of a contiguous CUDA tensor of dtype with n elements or
+    more (a raw address or None as it is)."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {n} or more {dtype} is read, "
+                         f"not {tuple(t.shape)} {t.dtype} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _raw_stream(torch, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream if stream.__class__ is int else stream.cuda_stream
+
+
+def _workspace(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
 
 
 def pa_tree_workspace_bytes(n_seqs: int, max_blocks: int, max_q_len: int, desc: PoolDesc) -> int:
@@ -577,55 +602,48 @@ def pa_tree_attention(out, q, k_cache, v_cache, block_tables, ctx_lens, q_starts
     """Attention of drafted nodes: rows q_starts[s]..q_starts[s+1]-1 of q are
     the last positions of sequence s, each seeing the positions before the
     nodes, itself and its ancestors by ``parents`` (None: a chain)."""
-    n = int(ctx_lens.shape[0]) if n_seqs is None else int(n_seqs)
-    mb = int(block_tables.shape[1]) if max_blocks is None else int(max_blocks)
-    rows = min(int(q.shape[0]), int(out.shape[0])) if q_rows is None else int(q_rows)
-    _need_dtype("float16", out=out, q=q, k_cache=k_cache, v_cache=v_cache)
-    _need_dtype("int32", block_tables=block_tables, ctx_lens=ctx_lens, q_starts=q_starts,
-                parents=parents)
-    _need_elems(rows * desc.num_heads * desc.head_dim, q=q, out=out)
-    _need_elems(n, ctx_lens=ctx_lens)
-    _need_elems(n + 1, q_starts=q_starts)
-    _need_elems(n * mb, block_tables=block_tables)
-    _need_elems(rows, parents=parents)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.pa_tree_attention(_dev(out), _dev(q), _dev(k_cache), _dev(v_cache),
-                                  _dev(block_tables), _dev(ctx_lens), _dev(q_starts),
-                                  _dev(parents), n, mb, int(max_q_len), rows,
-                                  ctypes.c_float(scale), _dev(workspace), ws_bytes, _dev(status),
-                                  desc.ref, _stream(stream)))
-
-
-_PROB_DTYPES = {"torch.float32": PA_DTYPE_F32, "torch.float16": PA_DTYPE_F16,
-                "torch.bfloat16": PA_DTYPE_BF16}
+    torch = _torch or _load_torch()
+    f16, i32 = torch.float16, torch.int32
+    n = ctx_lens.shape[0] if n_seqs is None else int(n_seqs)
+    mb = block_tables.shape[1] if max_blocks is None else int(max_blocks)
+    rows = min(q.shape[0], out.shape[0]) if q_rows is None else int(q_rows)
+    c = desc.c
+    width = c.num_heads * c.head_dim
+    cache = c.num_blocks * c.block_size * width
+    _check(_lib.pa_tree_attention(
+        _arg("out", out, f16, rows * width), _arg("q", q, f16, rows * width),
+        _arg("k_cache", k_cache, f16, cache), _arg("v_cache", v_cache, f16, cache),
+        _arg("block_tables", block_tables, i32, n * mb), _arg("ctx_lens", ctx_lens, i32, n),
+        _arg("q_starts", q_starts, i32, n + 1), _arg("parents", parents, i32, rows), n, mb,
+        max_q_len, rows, scale, _dev(workspace), _workspace(workspace), _arg("status", status, i32, 1),
+        desc.ref, _raw_stream(torch, stream)))
 
 
 def pa_verify_draft(path, path_lens, next_tokens, target_probs, draft_probs, draft_tokens,
                     parents, q_starts, u_accept, u_sample, max_q_len: int | None = None,
                     status=None, stream=None, n_seqs: int | None = None) -> None:
     """Accepted path, its length and the next token of every sequence from the
-    target's and the drafter's probabilities ([rows, vocab]; draft_probs None:
-    tokens picked outright) and given uniform numbers.  ``path`` is
-    int32 [n_seqs, max_q_len]."""
-    n = int(u_sample.shape[0]) if n_seqs is None else int(n_seqs)
-    mq = int(path.shape[1]) if max_q_len is None else int(max_q_len)
-    rows, vocab = (int(x) for x in target_probs.shape)
-    kind = str(target_probs.dtype)
-    if kind not in _PROB_DTYPES:
+    target's and the drafter's probabilities ([rows, vocab] float32, float16 or
+    bfloat16; draft_probs None: tokens picked outright) and given uniform
+    numbers.  ``path`` is int32 [n_seqs, max_q_len]."""
+    torch = _torch or _load_torch()
+    f32, i32 = torch.float32, torch.int32
+    n = u_sample.shape[0] if n_seqs is None else int(n_seqs)
+    mq = path.shape[1] if max_q_len is None else int(max_q_len)
+    rows, vocab = target_probs.shape
+    kind = target_probs.dtype
+    code = (PA_DTYPE_F32 if kind is f32 else PA_DTYPE_F16 if kind is torch.float16 else
+            PA_DTYPE_BF16 if kind is torch.bfloat16 else -1)
+    if code < 0:
         raise ValueError(f"target_probs is {kind}: float32, float16 or bfloat16 expected")
-    _need_dtype(kind[6:], draft_probs=draft_probs)
-    _need_dtype("int32", path=path, path_lens=path_lens, next_tokens=next_tokens,
-                draft_tokens=draft_tokens, parents=parents, q_starts=q_starts)
-    _need_dtype("float32", u_accept=u_accept, u_sample=u_sample)
-    _need_elems(rows * vocab, draft_probs=draft_probs)
-    _need_elems(rows, draft_tokens=draft_tokens, parents=parents, u_accept=u_accept)
-    _need_elems(n, path_lens=path_lens, next_tokens=next_tokens, u_sample=u_sample)
-    _need_elems(n + 1, q_starts=q_starts)
-    _need_elems(n * mq, path=path)
-    _check(_lib.pa_verify_draft(_dev(path), _dev(path_lens), _dev(next_tokens), _dev(target_probs),
-                                _dev(draft_probs), _PROB_DTYPES[kind], _dev(draft_tokens),
-                                _dev(parents), _dev(q_starts), _dev(u_accept), _dev(u_sample), n, mq,
-                                rows, vocab, _dev(status), _stream(stream)))
+    _check(_lib.pa_verify_draft(
+        _arg("path", path, i32, n * mq), _arg("path_lens", path_lens, i32, n),
+        _arg("next_tokens", next_tokens, i32, n), _arg("target_probs", target_probs, kind, 0),
+        _arg("draft_probs", draft_probs, kind, rows * vocab), code,
+        _arg("draft_tokens", draft_tokens, i32, rows), _arg("parents", parents, i32, rows),
+        _arg("q_starts", q_starts, i32, n + 1), _arg("u_accept", u_accept, f32, rows),
+        _arg("u_sample", u_sample, f32, n), n, mq, rows, vocab, _arg("status", status, i32, 1),
+        _raw_stream(torch, stream)))
 
 
 def pa_decode_weights_workspace_bytes(n_seqs: int, max_blocks: int, desc: PoolDesc) -> int:
@@ -639,24 +657,23 @@ def pa_decode_attention_weights(out, weights_out, weights_in, q, k_cache, v_cach
     """pa_decode_attention that adds each position's weight to weights_in
     (float32 [n_seqs, num_heads, weight_len], None: zeros) into weights_out,
     which may be the same tensor."""
-    n = int(q.shape[0]) if n_seqs is None else int(n_seqs)
-    mb = int(block_tables.shape[1]) if max_blocks is None else int(max_blocks)
-    wl = int(weights_out.shape[-1])
-    _need_dtype("float16", out=out, q=q, k_cache=k_cache, v_cache=v_cache)
-    _need_dtype("float32", weights_out=weights_out, weights_in=weights_in)
-    _need_dtype("int32", block_tables=block_tables, ctx_lens=ctx_lens)
-    _need_elems(n * desc.num_heads * desc.head_dim, q=q, out=out)
-    _need_elems(n * desc.num_heads * wl, weights_out=weights_out, weights_in=weights_in)
-    _need_elems(n, ctx_lens=ctx_lens)
-    _need_elems(n * mb, block_tables=block_tables)
-    if weights_in is not None and int(weights_in.shape[-1]) != wl:
+    torch = _torch or _load_torch()
+    f16, f32, i32 = torch.float16, torch.float32, torch.int32
+    n = q.shape[0] if n_seqs is None else int(n_seqs)
+    mb = block_tables.shape[1] if max_blocks is None else int(max_blocks)
+    wl = weights_out.shape[-1]
+    if weights_in is not None and weights_in.shape[-1] != wl:
         raise ValueError("weights_in and weights_out differ in length")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.pa_decode_attention_weights(_dev(out), _dev(weights_out), _dev(weights_in), wl,
-                                            _dev(q), _dev(k_cache), _dev(v_cache),
-                                            _dev(block_tables), _dev(ctx_lens), n, mb,
-                                            ctypes.c_float(scale), _dev(workspace), ws_bytes,
-                                            _dev(status), desc.ref, _stream(stream)))
+    c = desc.c
+    width = c.num_heads * c.head_dim
+    cache, sums = c.num_blocks * c.block_size * width, n * c.num_heads * wl
+    _check(_lib.pa_decode_attention_weights(
+        _arg("out", out, f16, n * width), _arg("weights_out", weights_out, f32, sums),
+        _arg("weights_in", weights_in, f32, sums), wl, _arg("q", q, f16, n * width),
+        _arg("k_cache", k_cache, f16, cache), _arg("v_cache", v_cache, f16, cache),
+        _arg("block_tables", block_tables, i32, n * mb), _arg("ctx_lens", ctx_lens, i32, n), n, mb,
+        scale, _dev(workspace), _workspace(workspace), _arg("status", status, i32, 1), desc.ref,
+        _raw_stream(torch, stream)))
 
 
 def pa_evict_select(keep, keep_lens, weights_out, weights_in, ctx_lens, budget: int, recent: int,
@@ -665,18 +682,18 @@ def pa_evict_select(keep, keep_lens, weights_out, weights_in, ctx_lens, budget: 
     with the largest weights_in, ``budget`` in all, into keep (int32
     [n_seqs, num_heads, budget], ascending, padded with -1); their weights into
     weights_out, which may be weights_in."""
-    n = int(ctx_lens.shape[0]) if n_seqs is None else int(n_seqs)
-    heads, wl = int(weights_in.shape[1]), int(weights_in.shape[2])
-    if tuple(weights_out.shape[1:]) != (heads, wl):
+    torch = _torch or _load_torch()
+    f32, i32 = torch.float32, torch.int32
+    n = ctx_lens.shape[0] if n_seqs is None else int(n_seqs)
+    _, heads, wl = weights_in.shape
+    if weights_out.shape[1:] != weights_in.shape[1:]:
         raise ValueError("weights_in and weights_out differ in shape")
-    _need_dtype("int32", keep=keep, keep_lens=keep_lens, ctx_lens=ctx_lens)
-    _need_dtype("float32", weights_out=weights_out, weights_in=weights_in)
-    _need_elems(n * heads * max(int(budget), 0), keep=keep)
-    _need_elems(n * heads * wl, weights_out=weights_out, weights_in=weights_in)
-    _need_elems(n, keep_lens=keep_lens, ctx_lens=ctx_lens)
-    _check(_lib.pa_evict_select(_dev(keep), _dev(keep_lens), _dev(weights_out), _dev(weights_in), wl,
-                                _dev(ctx_lens), n, heads, int(budget), int(recent), _dev(status),
-                                _stream(stream)))
+    sums = n * heads * wl
+    _check(_lib.pa_evict_select(
+        _arg("keep", keep, i32, n * heads * budget), _arg("keep_lens", keep_lens, i32, n),
+        _arg("weights_out", weights_out, f32, sums), _arg("weights_in", weights_in, f32, sums), wl,
+        _arg("ctx_lens", ctx_lens, i32, n), n, heads, budget, recent,
+        _arg("status", status, i32, 1), _raw_stream(torch, stream)))
 
 
 def pa_compact_kv(k_caches, v_caches, src_tables, dst_tables, src_lens, keep, keep_lens,
@@ -685,27 +702,27 @@ def pa_compact_kv(k_caches, v_caches, src_tables, dst_tables, src_lens, keep, ke
     """Every layer's K/V rows at positions first + keep[s, h, j] (src_tables)
     move to first + j (dst_tables).  keep: int32 [n_seqs, 1 or num_heads, n]
     or [n_seqs, n] (one list for all heads)."""
+    torch = _torch or _load_torch()
+    f16, i32 = torch.float16, torch.int32
     L = len(k_caches)
-    n = int(keep_lens.shape[0]) if n_seqs is None else int(n_seqs)
-    mb = int(src_tables.shape[1])
-    heads = int(keep.shape[1]) if keep.dim() == 3 else 1
-    stride = int(keep.shape[-1])
+    n = keep_lens.shape[0] if n_seqs is None else int(n_seqs)
+    mb = src_tables.shape[1]
+    heads = keep.shape[1] if keep.dim() == 3 else 1
+    stride = keep.shape[-1]
     if len(v_caches) != L:
         raise ValueError("k_caches and v_caches differ in length")
-    if int(dst_tables.shape[1]) != mb:
+    if dst_tables.shape[1] != mb:
         raise ValueError("src_tables and dst_tables differ in width")
-    for cache in (*k_caches, *v_caches):
-        _need_dtype("float16", cache=cache)
-    _need_dtype("int32", src_tables=src_tables, dst_tables=dst_tables, src_lens=src_lens,
-                keep=keep, keep_lens=keep_lens, first=first)
-    _need_elems(n * mb, src_tables=src_tables, dst_tables=dst_tables)
-    _need_elems(n, src_lens=src_lens, keep_lens=keep_lens, first=first)
-    _need_elems(n * heads * stride, keep=keep)
-    kp = (ctypes.c_void_p * L)(*[_dev(x) for x in k_caches])
-    vp = (ctypes.c_void_p * L)(*[_dev(x) for x in v_caches])
-    _check(_lib.pa_compact_kv(kp, vp, L, _dev(src_tables), _dev(dst_tables), _dev(src_lens),
-                              _dev(first), _dev(keep), _dev(keep_lens), heads, stride, n, mb,
-                              desc.ref, _dev(status), _stream(stream)))
+    c = desc.c
+    cache = c.num_blocks * c.block_size * c.num_heads * c.head_dim
+    kp = (ctypes.c_void_p * L)(*[_arg("k_caches", x, f16, cache) for x in k_caches])
+    vp = (ctypes.c_void_p * L)(*[_arg("v_caches", x, f16, cache) for x in v_caches])
+    _check(_lib.pa_compact_kv(
+        kp, vp, L, _arg("src_tables", src_tables, i32, n * mb),
+        _arg("dst_tables", dst_tables, i32, n * mb), _arg("src_lens", src_lens, i32, n),
+        _arg("first", first, i32, n), _arg("keep", keep, i32, n * heads * stride),
+        _arg("keep_lens", keep_lens, i32, n), heads, stride, n, mb, desc.ref,
+        _arg("status", status, i32, 1), _raw_stream(torch, stream)))
 
 
 def pa_selftest_bounded_wait(status, stream=None) -> None:

@@ -72,7 +72,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kHeaderBytes = 256;    // workspace head: unit ticket, number of cut sequences
+constexpr int kHeaderBytes = 256;    // workspace head: number of cut sequences
 constexpr int kUnitSlots = 3;        // units a CTA has open
 constexpr int kTile = 128;           // tokens of a tile: the lanes of tensor memory
 constexpr float kRescaleLog2 = 8.f;  // tensor-memory kernel: how far a row's maximum may pass its reference
@@ -84,7 +84,7 @@ struct TreeParams {
     const int32_t *ctx_lens;
     const int32_t *q_starts;   // NULL (weights form): one query a sequence
     const int32_t *parents;    // NULL: a chain
-    int32_t *header;           // [0] unit tickets, [1] cut sequences
+    int32_t *header;           // [0] cut sequences
     int4 *cut;                 // [cap] cut sequences: s, first part, parts, rows
     float2 *ws_ml;             // [cap][H][NR] (max, sum) of a part's rows
     float *ws_acc;             // [cap][H][NR][D] unnormalised output
@@ -318,7 +318,7 @@ __device__ void make_plan(const TreeParams &p, int32_t *pre, int32_t *len, uint1
     __syncthreads();
     if (blockIdx.x == 0) {   // for the kernels that join the parts
         const int n_cut = vars[1];
-        if (tid == 0) p.header[1] = n_cut;
+        if (tid == 0) p.header[0] = n_cut;
         for (int i = tid; i < n_cut; i += (int)blockDim.x) {
             const int s = order[i];
             const SeqRows r = rows_of<SCORES>(p, s, false);
@@ -573,9 +573,9 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
             ok = __all_sync(kAll, ok);
             return ok;
         };
-        int t_next = 0;
+        // Units in order of size, back and forth over the CTAs.
+        const int G = gridDim.x;
         Pending cur = prepare(blockIdx.x);
-        if (lane == 0) t_next = (int)gridDim.x + atomicAdd(p.header, 1);
         while (true) {
             const bool last = cur.ticket >= n_units;     // one more descriptor: the end
             const int slot = k_unit % kUnitSlots, slot_use = k_unit / kUnitSlots;
@@ -601,9 +601,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
             if (lane == 0) mbar_arrive(bar_unit + 8 * slot);
             ++k_unit;
             if (last) break;
-            const int tn = __shfl_sync(kAll, t_next, 0);
-            if (lane == 0 && tn < n_units) t_next = (int)gridDim.x + atomicAdd(p.header, 1);
-            const Pending nxt = prepare(tn);
+            const Pending nxt = prepare(k_unit * G + (k_unit & 1 ? G - 1 - (int)blockIdx.x : (int)blockIdx.x));
             const int32_t *trow = p.block_tables + (size_t)cur.s * p.max_blocks + cur.b0;
             int tbl = cur.tbl;
             for (int b = 0; b < cur.nb; b += bps) {
@@ -988,7 +986,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p, int 
     constexpr int DL = D / 32;
     const int lane = threadIdx.x & 31, H = p.num_heads;
     wait_for_launch_before();
-    const long long items = (long long)p.header[1] * H * NR;
+    const long long items = (long long)p.header[0] * H * NR;
     const long long step = (long long)gridDim.x * 8;
     for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += step) {
         const int row = (int)(it % NR);
@@ -1238,10 +1236,8 @@ int launch_tree(TreeParams p, const TreeMaps &maps, const char *who, cudaStream_
     static_assert((227 * 1024 - TreeCfg<128, 64>::PLAN - 10 * PA_TREE_MAX_SEQS - 8 - 1024 - TreeCfg<128, 64>::Q_BYTES -
                    2 * TreeCfg<128, 64>::P_BYTES) / TreeCfg<128, 64>::HALF >= kMinStages,
                   "room beside the largest batch's plan");
-    cudaError_t e = cudaMemsetAsync(p.header, 0, 8, st);
-    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: memset: %s", who, cudaGetErrorString(e));
     kern<<<sm_count(), Cfg::THREADS, Cfg::bytes(p.n_seqs, p.stages), st>>>(p, maps);
-    e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return PA_OK;
 }
