@@ -19,18 +19,22 @@ constexpr unsigned kAll = 0xffffffffu;
 //
 // For one (sequence, head): the last `recent` of ctx positions and, of the
 // others, the budget - recent with the largest sums (ties to the lowest
-// position), in ascending order.  One CTA finds the sum of the last one kept
-// by radix selection on order-preserving keys, 11 + 11 + 10 bits (the first
-// digit holds sign, exponent and 2 mantissa bits, so the sums of one head
-// spread over many bins and the shared-memory counters do not queue up), then
-// writes the kept positions in order with one counting and one writing sweep,
-// each warp over a contiguous span.  It reads 4 bytes a position from memory
-// once: contexts up to kCached positions stay in shared memory, longer ones
-// are re-read through L2.
+// position), in ascending order.  One CTA finds the sum of the last one kept on
+// order-preserving keys: a histogram of their first 11 bits (sign, exponent and
+// 2 mantissa bits, so the sums of one head spread over many bins and the
+// shared-memory counters do not queue up), then, where the bin that holds it
+// has few keys, each of those counts the ones above it; where it has many
+// (equal sums, mostly) two more histograms.  Then the kept positions are written
+// in order, with one counting and one writing sweep, each warp over a contiguous
+// span.  It reads 4 bytes a position from memory once: contexts up to kCached
+// positions stay in shared memory, longer ones are re-read through L2.  Bound
+// by the barriers between these steps, so short rows take small CTAs, several
+// an SM.
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kCached = 24576;       // positions of a row kept in shared memory (96 KB)
+constexpr int kFew = 512;            // keys of a bin that are ranked one against another
+constexpr int kShort = 4096;         // positions up to which a CTA has 256 threads, else 1024
+constexpr int kCached = 49152;       // positions of a row kept in shared memory (192 KB)
 
 // Larger sums have larger keys; -0 counts as 0, NaN as less than everything.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -48,12 +52,13 @@ struct SelectParams {
     int32_t *status;
 };
 
-template <bool CACHED>
+template <bool CACHED, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams a) {
+    constexpr int kSelWarps = kSelThreads / 32;
     extern __shared__ float row_sh[];
-    __shared__ uint32_t bins[kBins];
+    __shared__ uint32_t bins[kBins];   // after a histogram: the few keys of the bin
     __shared__ uint32_t part[kSelWarps], part2[kSelWarps];
-    __shared__ uint32_t found[2];      // digit, and how many of it are still wanted
+    __shared__ uint32_t found[4];      // digit, how many of it are still wanted, how many there are; listed
     const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ctx = max(a.ctx_lens[s], 0), budget = a.budget;
     const size_t sh_row = (size_t)s * a.num_heads + h;
@@ -76,25 +81,36 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
         return;
     }
     const int old = ctx - a.recent, heavy = budget - a.recent;   // 0 <= heavy < old
-    if (CACHED) {
-        for (int j = tid; j < ctx; j += kSelThreads) row_sh[j] = w[j];
-        __syncthreads();
-    }
     auto at = [&](int j) { return CACHED ? row_sh[j] : w[j]; };
 
-    // ---- the key of the last kept position, and how many of that key are kept
-    uint32_t prefix = 0, mask = 0;
-    int want = heavy;
+    // ---- the last kept position in the order of sums: its key and position
+    // (kept: larger keys, and the same key up to that position), and how many
+    // each warp's span keeps
+    const int per = (old + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
+    const int lo = min(old, warp * per), hi = min(old, lo + per);
+    uint32_t last = 0;
+    int cut = -1;
     if (heavy > 0) {
-#pragma unroll
-        for (int pass = 0; pass < 3; ++pass) {
+        uint32_t prefix = 0, mask = 0;
+        int want = heavy;
+        bool few = false;
+#pragma unroll 1
+        for (int pass = 0; pass < 3 && !few; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const int nb = pass == 2 ? 1024 : 2048;
             for (int b = tid; b < nb; b += kSelThreads) bins[b] = 0;
             __syncthreads();
-            for (int j = tid; j < old; j += kSelThreads) {
-                const uint32_t key = key_of(at(j));
-                if ((key & mask) == prefix) atomicAdd(&bins[(key >> shift) & (nb - 1)], 1u);
+            if (pass == 0) {
+                for (int j = tid; j < ctx; j += kSelThreads) {
+                    const float x = w[j];
+                    if (CACHED) row_sh[j] = x;
+                    if (j < old) atomicAdd(&bins[key_of(x) >> 21], 1u);
+                }
+            } else {
+                for (int j = tid; j < old; j += kSelThreads) {
+                    const uint32_t key = key_of(at(j));
+                    if ((key & mask) == prefix) atomicAdd(&bins[(key >> shift) & (nb - 1)], 1u);
+                }
             }
             __syncthreads();
             // bins from the top: thread t owns the bins [nb - (t+1) e, nb - t e)
@@ -118,51 +134,96 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
                     if ((int)(run + bins[b]) >= want) {
                         found[0] = (uint32_t)b;
                         found[1] = (uint32_t)want - run;
+                        found[2] = bins[b];
                         break;
                     }
                     run += bins[b];
                 }
+                found[3] = 0;
             }
             __syncthreads();
             prefix |= found[0] << shift;
             mask |= (uint32_t)(nb - 1) << shift;
             want = (int)found[1];
+            few = found[2] <= kFew;
+        }
+        const uint32_t many = found[2];
+        __syncthreads();
+        uint32_t more = 0, same = 0;       // in this warp's span: surely kept; of the bin
+        if (few) {
+            // the bin's keys and positions; each counts the ones before it in order
+            uint32_t *keys = bins, *places = bins + kFew;
+            for (int j0 = lo; j0 < hi; j0 += 32) {
+                const int j = j0 + lane;
+                const uint32_t key = j < hi ? key_of(at(j)) : 0u;
+                const bool in = j < hi && (key & mask) == prefix;
+                more += __popc(__ballot_sync(kAll, j < hi && (key & mask) > prefix));
+                if (in) {
+                    const uint32_t i = atomicAdd(&found[3], 1u);
+                    keys[i] = key;
+                    places[i] = (uint32_t)j;
+                }
+            }
             __syncthreads();
+            for (uint32_t i = tid; i < many; i += kSelThreads) {
+                const uint32_t key = keys[i], place = places[i];
+                int ahead = 0;
+                for (uint32_t k = 0; k < many; ++k)
+                    ahead += keys[k] > key || (keys[k] == key && places[k] < place);
+                if (ahead == want - 1) {
+                    found[0] = key;
+                    found[1] = place;
+                }
+            }
+            __syncthreads();
+            last = found[0];
+            cut = (int)found[1];
+            for (uint32_t i = lane; i < many; i += 32)
+                same += (keys[i] > last || (keys[i] == last && (int)places[i] <= cut)) && (int)places[i] >= lo &&
+                        (int)places[i] < hi;
+            more += __reduce_add_sync(kAll, same);
+        } else {
+            // a key that many positions share: the want-th of them in order
+            last = prefix;
+            for (int j0 = lo; j0 < hi; j0 += 32) {
+                const int j = j0 + lane;
+                const uint32_t key = j < hi ? key_of(at(j)) : 0u;
+                more += __popc(__ballot_sync(kAll, j < hi && key > last));
+                same += __popc(__ballot_sync(kAll, j < hi && key == last));
+            }
+            if (lane == 0) part2[warp] = same;
+            __syncthreads();
+            int ahead = 0;
+            for (int k = 0; k < warp; ++k) ahead += (int)part2[k];
+            if (ahead < want && want <= ahead + (int)same) {      // it lies in this warp's span
+                for (int j0 = lo, run = ahead; j0 < hi; j0 += 32) {
+                    const int j = j0 + lane;
+                    const unsigned eq = __ballot_sync(kAll, j < hi && key_of(at(min(j, hi - 1))) == last);
+                    if (run < want && want <= run + __popc(eq)) {
+                        if (((eq >> lane) & 1) && run + __popc(eq & ((2u << lane) - 1)) == want) found[1] = (uint32_t)j;
+                    }
+                    run += __popc(eq);
+                }
+            }
+            __syncthreads();
+            cut = (int)found[1];
+            more += (uint32_t)max(0, min((int)same, want - ahead));
         }
+        if (lane == 0) part[warp] = more;
+        __syncthreads();
+    } else if (CACHED) {
+        for (int j = tid; j < ctx; j += kSelThreads) row_sh[j] = w[j];
+        __syncthreads();
     }
-    const uint32_t last = prefix;
 
-    // ---- kept positions in order: count by warp, then write
-    const int per = (old + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
-    const int lo = min(old, warp * per), hi = min(old, lo + per);
-    uint32_t more = 0, same = 0;
+    // ---- kept positions in order
     if (heavy > 0) {
+        uint32_t out = 0;
+        for (int k = 0; k < warp; ++k) out += part[k];
         for (int j0 = lo; j0 < hi; j0 += 32) {
             const int j = j0 + lane;
             const uint32_t key = j < hi ? key_of(at(j)) : 0u;
-            more += __popc(__ballot_sync(kAll, j < hi && key > last));
-            same += __popc(__ballot_sync(kAll, j < hi && key == last));
-        }
-    }
-    if (lane == 0) {
-        part[warp] = more;
-        part2[warp] = same;
-    }
-    __syncthreads();
-    uint32_t same_run = 0, out = 0;
-    for (int k = 0; k < warp; ++k) {
-        const uint32_t left = (uint32_t)want > same_run ? (uint32_t)want - same_run : 0u;
-        out += part[k] + min(part2[k], left);
-        same_run += part2[k];
-    }
-    if (heavy > 0) {
-        for (int j0 = lo; j0 < hi; j0 += 32) {
-            const int j = j0 + lane;
-            const uint32_t key = j < hi ? key_of(at(j)) : 0u;
-            const unsigned eq = __ballot_sync(kAll, j < hi && key == last);
-            const bool tie = j < hi && key == last &&
-                             same_run + __popc(eq & ((1u << lane) - 1)) < (uint32_t)want;
-            const bool take = (j < hi && key > last) || tie;
+            const bool take = j < hi && (key > last || (key == last && j <= cut));
             const unsigned m = __ballot_sync(kAll, take);
             if (take) {
                 const uint32_t o = out + __popc(m & ((1u << lane) - 1));
@@ -170,7 +231,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
                 if (CACHED) wo[o] = row_sh[j];
             }
             out += __popc(m);
-            same_run += __popc(eq);
         }
     }
     for (int j = tid; j < a.recent; j += kSelThreads) {
@@ -198,42 +258,48 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
 // at position first + keep[j], keep strictly ascending: keep[j] >= j, so in
 // place every row is read before anything is written over it as long as reads
 // run ahead of writes in order.  A CTA owns whole columns (16-byte vectors of
-// a head's rows) and walks the rows in chunks: all loads of a chunk, a
-// barrier, all its stores.  Bound by the bytes: each kept row is read and
-// written once; rows already in place are skipped.
+// a head's rows) and walks the rows in chunks: where the chunk's rows lie, all
+// loads, all stores.  Bound by the bytes: each kept row is read and written
+// once; rows already in place are skipped.  Two forms:
+//   * a list for each head, or a long one: a head of a cache a CTA, 16 threads a
+//     row (D = 128) and so many rows at once, a barrier between loads and stores;
+//   * a short list for all heads (accepted drafts; many layers): a
+//     thread has a column of all heads' rows to itself, needs no barrier, and
+//     moves keys and values of several layers by the same row numbers (finding
+//     them takes longer than moving a row).
 
-constexpr int kMoveThreads = 256, kUnroll = 8;
+constexpr int kMoveThreads = 256;
 constexpr int kMaxMoveLayers = 128;
 constexpr int kMaxChunk = 512;       // rows of a chunk
+constexpr int kShortList = 64;       // entries up to which one list for all heads moves by columns
 
 struct CompactParams {
     const int32_t *src_tables, *dst_tables, *src_lens, *first, *keep, *keep_lens;
     int32_t num_heads, keep_heads, keep_stride, max_blocks, num_blocks, bshift, row_shift;
     int32_t cols, rows, chunk;       // columns and rows a pass of the CTA covers; rows of a chunk
+    int32_t layers, each;            // layers in all, and of a CTA (shared lists)
     int32_t *status;
-    uint4 *cache[2 * kMaxMoveLayers];
+    uint4 *cache[2 * kMaxMoveLayers];   // keys and values of layer 0, 1, ..
 };
 
+template <bool SHARED>
 __global__ void __launch_bounds__(kMoveThreads) compact_kv_kernel(const __grid_constant__ CompactParams a) {
-    __shared__ long long from[2][kMaxChunk], to[2][kMaxChunk];   // row numbers in the cache, -1: none
+    constexpr int kUnroll = SHARED ? 4 : 8;
+    __shared__ long long from[2][SHARED ? kUnroll : kMaxChunk], to[2][SHARED ? kUnroll : kMaxChunk];   // row numbers, -1: none
     const int s = blockIdx.y, tid = threadIdx.x;
-    // blockIdx.x: (head of the keep list, group of columns)
     const int vec = 1 << a.row_shift;                   // vectors of a row
-    const int heads_each = a.num_heads / a.keep_heads;  // heads that share a list: 1 or all
-    const int col_groups = (heads_each * vec + a.cols - 1) / a.cols;
-    const int kh = blockIdx.x / col_groups, cg = blockIdx.x - kh * col_groups;
-    uint4 *cache = a.cache[blockIdx.z];
+    const int H = a.num_heads, B = 1 << a.bshift, heads = SHARED ? H : 1;   // heads of a list
+    // blockIdx.x: group of columns, or head
+    const int kh = SHARED ? 0 : blockIdx.x, cg = SHARED ? blockIdx.x : 0;
     const int len = a.keep_lens[s], ctx = a.src_lens[s], first = a.first ? a.first[s] : 0;
-    const bool tell = tid == 0 && blockIdx.x == 0 && blockIdx.z == 0;
     if (len <= 0) return;
     if (len > a.keep_stride || first < 0) {
-        if (tell) report(a.status, PA_ERR_INVALID_ARG);
+        if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0) report(a.status, PA_ERR_INVALID_ARG);
         return;
     }
-    const int32_t *keep = a.keep + ((size_t)s * a.keep_heads + kh) * a.keep_stride;
+    const int32_t *keep = a.keep + ((size_t)s * a.keep_heads + (a.keep_heads > 1 ? kh : 0)) * a.keep_stride;
     const int32_t *src = a.src_tables + (size_t)s * a.max_blocks;
     const int32_t *dst = a.dst_tables + (size_t)s * a.max_blocks;
-    const int B = 1 << a.bshift, H = a.num_heads;
 
     // Rows (of head kh, or of head 0 of all) that row j of the list moves between.
     auto plan = [&](int buf, int j0) {
@@ -252,8 +318,8 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kv_kernel(const __grid_c
                     if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) {
                         report(a.status, PA_ERR_BAD_BLOCK);
                     } else if (sb != db || sp != dp) {
-                        f = (((long long)sb * H + kh * heads_each) << a.bshift) + (sp & (B - 1));
-                        t = (((long long)db * H + kh * heads_each) << a.bshift) + (dp & (B - 1));
+                        f = (((long long)sb * H + kh) << a.bshift) + (sp & (B - 1));
+                        t = (((long long)db * H + kh) << a.bshift) + (dp & (B - 1));
                     }
                 }
             }
@@ -263,30 +329,46 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kv_kernel(const __grid_c
     };
     const int c = tid % a.cols, r = tid / a.cols;
     const int col = cg * a.cols + c;                    // vector of the row, over the list's heads
-    const bool mine = col < heads_each * vec && r < a.rows;
+    const bool mine = col < heads * vec && r < a.rows;
     // column col is vector col % vec of head col / vec
     const long long col_off =
         ((long long)(col >> a.row_shift) << (a.bshift + a.row_shift)) + (col & (vec - 1));
+    auto load = [&](const uint4 *cache, int buf, uint4 (&x)[kUnroll]) {
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            const int i = r + k * a.rows;
+            if (i < a.chunk && from[buf][i] >= 0) x[k] = cache[(from[buf][i] << a.row_shift) + col_off];
+        }
+    };
+    auto store = [&](uint4 *cache, int buf, const uint4 (&x)[kUnroll]) {
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            const int i = r + k * a.rows;
+            if (i < a.chunk && to[buf][i] >= 0) cache[(to[buf][i] << a.row_shift) + col_off] = x[k];
+        }
+    };
     plan(0, 0);
     __syncthreads();
     int buf = 0;
     for (int j0 = 0; j0 < len; j0 += a.chunk, buf ^= 1) {
         uint4 x[kUnroll];
-        if (mine) {
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int i = r + k * a.rows;
-                if (i < a.chunk && from[buf][i] >= 0) x[k] = cache[(from[buf][i] << a.row_shift) + col_off];
-            }
-        }
-        if (j0 + a.chunk < len) plan(buf ^ 1, j0 + a.chunk);
-        __syncthreads();
-        if (mine) {
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int i = r + k * a.rows;
-                if (i < a.chunk && to[buf][i] >= 0) cache[(to[buf][i] << a.row_shift) + col_off] = x[k];
-            }
+        if (SHARED) {
+            if (j0 + a.chunk < len) plan(buf ^ 1, j0 + a.chunk);
+            const int l1 = min(a.layers, (int)(blockIdx.z + 1) * a.each);
+            if (mine)
+                for (int l = blockIdx.z * a.each; l < l1; ++l) {
+                    uint4 y[kUnroll];
+                    load(a.cache[2 * l], buf, x);
+                    load(a.cache[2 * l + 1], buf, y);
+                    store(a.cache[2 * l], buf, x);
+                    store(a.cache[2 * l + 1], buf, y);
+                }
+        } else {
+            uint4 *cache = a.cache[blockIdx.z];
+            if (mine) load(cache, buf, x);
+            if (j0 + a.chunk < len) plan(buf ^ 1, j0 + a.chunk);
+            __syncthreads();
+            if (mine) store(cache, buf, x);
         }
         __syncthreads();
     }
@@ -315,14 +397,16 @@ int launch_evict_select(int32_t *keep, int32_t *keep_lens, float *weights_out, c
     const dim3 grid((unsigned)num_heads, (unsigned)n_seqs);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (weight_len <= kCached) {
-        const int bytes = weight_len * 4;
-        if (bytes > 32 * 1024)
-            e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const int bytes = weight_len * 4;
+    if (weight_len <= kShort) {
+        evict_select_kernel<true, 256><<<grid, 256, bytes, st>>>(a);
+    } else if (weight_len <= kCached) {
+        if (bytes > 32 * 1024)       // (beside 8 KB of counters)
+            e = cudaFuncSetAttribute(evict_select_kernel<true, 1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kCached * 4);
-        if (e == cudaSuccess) evict_select_kernel<true><<<grid, kSelThreads, bytes, st>>>(a);
+        if (e == cudaSuccess) evict_select_kernel<true, 1024><<<grid, 1024, bytes, st>>>(a);
     } else {
-        evict_select_kernel<false><<<grid, kSelThreads, 0, st>>>(a);
+        evict_select_kernel<false, 1024><<<grid, 1024, 0, st>>>(a);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
@@ -373,14 +457,26 @@ int launch_compact_kv(void *const *k_caches, void *const *v_caches, int32_t num_
     while ((1 << a.bshift) < d->block_size) ++a.bshift;
     while ((8 << a.row_shift) < d->head_dim) ++a.row_shift;
     a.status = status;
-    const int64_t columns = (int64_t)(d->num_heads / keep_heads) << a.row_shift;
-    a.cols = (int)std::min<int64_t>(columns, kMoveThreads);
-    a.rows = kMoveThreads / a.cols;
-    a.chunk = std::min(kMaxChunk, a.rows * kUnroll);
-    const int64_t gx = (columns + a.cols - 1) / a.cols * keep_heads;
-    if (gx > INT32_MAX) return fail(PA_ERR_INVALID_ARG, "%s: num_heads * head_dim too large", who);
-    compact_kv_kernel<<<dim3((unsigned)gx, (unsigned)n_seqs, (unsigned)(2 * num_layers)), kMoveThreads, 0,
-                        static_cast<cudaStream_t>(stream)>>>(a);
+    a.layers = num_layers;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned S = (unsigned)n_seqs;
+    if (keep_heads > 1 || keep_stride > kShortList) {
+        a.cols = 1 << a.row_shift;
+        a.rows = kMoveThreads / a.cols;
+        a.chunk = std::min(kMaxChunk, a.rows * 8);
+        compact_kv_kernel<false><<<dim3((unsigned)d->num_heads, S, (unsigned)(2 * num_layers)), kMoveThreads, 0, st>>>(a);
+    } else {
+        const int64_t columns = (int64_t)d->num_heads << a.row_shift;
+        a.cols = kMoveThreads;
+        a.rows = 1;
+        a.chunk = 4;
+        const int64_t gx = (columns + a.cols - 1) / a.cols;
+        if (gx > INT32_MAX) return fail(PA_ERR_INVALID_ARG, "%s: num_heads * head_dim too large", who);
+        // as many layers a CTA as leave some 30 CTAs an SM
+        a.each = (int)std::max<int64_t>(1, std::min<int64_t>(num_layers, gx * n_seqs * num_layers / 4608));
+        compact_kv_kernel<true><<<dim3((unsigned)gx, S, (unsigned)((num_layers + a.each - 1) / a.each)), kMoveThreads, 0,
+                                  st>>>(a);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return PA_OK;
