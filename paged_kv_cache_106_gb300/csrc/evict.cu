@@ -56,7 +56,7 @@ template <bool CACHED, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams a) {
     constexpr int kSelWarps = kSelThreads / 32;
     extern __shared__ float row_sh[];
-    __shared__ uint32_t bins[kBins];   // after a histogram: the few keys of the bin
+    __shared__ __align__(16) uint32_t bins[kBins];   // after a histogram: the few keys of the bin
     __shared__ uint32_t part[kSelWarps], part2[kSelWarps];
     __shared__ uint32_t found[4];      // digit, how many of it are still wanted, how many there are; listed
     const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -101,10 +101,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
             for (int b = tid; b < nb; b += kSelThreads) bins[b] = 0;
             __syncthreads();
             if (pass == 0) {
-                for (int j = tid; j < ctx; j += kSelThreads) {
-                    const float x = w[j];
-                    if (CACHED) row_sh[j] = x;
-                    if (j < old) atomicAdd(&bins[key_of(x) >> 21], 1u);
+                constexpr int kAtOnce = kSelThreads == 1024 ? 8 : 4;
+                for (int j0 = tid; j0 < ctx; j0 += kAtOnce * kSelThreads) {
+                    float x[kAtOnce];
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) x[k] = j0 + k * kSelThreads < ctx ? w[j0 + k * kSelThreads] : 0.f;
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) {
+                        const int j = j0 + k * kSelThreads;
+                        if (CACHED && j < ctx) row_sh[j] = x[k];
+                        if (j < old) atomicAdd(&bins[key_of(x[k]) >> 21], 1u);
+                    }
                 }
             } else {
                 for (int j = tid; j < old; j += kSelThreads) {
@@ -116,7 +123,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
             // bins from the top: thread t owns the bins [nb - (t+1) e, nb - t e)
             const int e = nb / kSelThreads;
             uint32_t mine = 0;
-            for (int k = 0; k < e; ++k) mine += bins[nb - 1 - (tid * e + k)];
+            if (e % 4 == 0) {
+                const uint4 *b4 = reinterpret_cast<const uint4 *>(bins + nb - (tid + 1) * e);
+                for (int k = 0; k < e / 4; ++k) mine += b4[k].x + b4[k].y + b4[k].z + b4[k].w;
+            } else {
+                for (int k = 0; k < e; ++k) mine += bins[nb - 1 - (tid * e + k)];
+            }
             uint32_t incl = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -151,37 +163,39 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
         __syncthreads();
         uint32_t more = 0, same = 0;       // in this warp's span: surely kept; of the bin
         if (few) {
-            // the bin's keys and positions; each counts the ones before it in order
-            uint32_t *keys = bins, *places = bins + kFew;
+            // the bin's positions in one number each, larger ones first in order;
+            // each counts the ones before it
+            unsigned long long *list = reinterpret_cast<unsigned long long *>(bins);
+            uint32_t above = 0;
             for (int j0 = lo; j0 < hi; j0 += 32) {
                 const int j = j0 + lane;
                 const uint32_t key = j < hi ? key_of(at(j)) : 0u;
                 const bool in = j < hi && (key & mask) == prefix;
-                more += __popc(__ballot_sync(kAll, j < hi && (key & mask) > prefix));
+                above += j < hi && (key & mask) > prefix;
                 if (in) {
-                    const uint32_t i = atomicAdd(&found[3], 1u);
-                    keys[i] = key;
-                    places[i] = (uint32_t)j;
+                    list[atomicAdd(&found[3], 1u)] = (unsigned long long)key << 32 | ~(uint32_t)j;
                 }
             }
             __syncthreads();
             for (uint32_t i = tid; i < many; i += kSelThreads) {
-                const uint32_t key = keys[i], place = places[i];
+                const unsigned long long mine = list[i];
                 int ahead = 0;
-                for (uint32_t k = 0; k < many; ++k)
-                    ahead += keys[k] > key || (keys[k] == key && places[k] < place);
+#pragma unroll 8
+                for (uint32_t k = 0; k < many; ++k) ahead += list[k] > mine;
                 if (ahead == want - 1) {
-                    found[0] = key;
-                    found[1] = place;
+                    found[0] = (uint32_t)(mine >> 32);
+                    found[1] = ~(uint32_t)mine;
                 }
             }
             __syncthreads();
             last = found[0];
             cut = (int)found[1];
-            for (uint32_t i = lane; i < many; i += 32)
-                same += (keys[i] > last || (keys[i] == last && (int)places[i] <= cut)) && (int)places[i] >= lo &&
-                        (int)places[i] < hi;
-            more += __reduce_add_sync(kAll, same);
+            const unsigned long long least = (unsigned long long)last << 32 | ~(uint32_t)cut;
+            for (uint32_t i = lane; i < many; i += 32) {
+                const int j = (int)~(uint32_t)list[i];
+                same += list[i] >= least && j >= lo && j < hi;
+            }
+            more = __reduce_add_sync(kAll, above + same);
         } else {
             // a key that many positions share: the want-th of them in order
             last = prefix;
