@@ -34,7 +34,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kBins = 2048;
 constexpr int kFew = 512;            // keys of a bin that are ranked one against another
 constexpr int kShort = 4096;         // positions up to which a CTA has 256 threads, else 1024
-constexpr int kCached = 49152;       // positions of a row kept in shared memory (192 KB)
+constexpr int kCached = 26624;       // positions of a row kept in shared memory (104 KB: two CTAs an SM)
 
 // Larger sums have larger keys; -0 counts as 0, NaN as less than everything.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -53,7 +53,7 @@ struct SelectParams {
 };
 
 template <bool CACHED, int kSelThreads>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams a) {
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectParams a) {
     constexpr int kSelWarps = kSelThreads / 32;
     extern __shared__ float row_sh[];
     __shared__ __align__(16) uint32_t bins[kBins];   // after a histogram: the few keys of the bin
@@ -82,6 +82,18 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     }
     const int old = ctx - a.recent, heavy = budget - a.recent;   // 0 <= heavy < old
     auto at = [&](int j) { return CACHED ? row_sh[j] : w[j]; };
+    // f(position, its key) over a warp's span, 32 positions at a time (all lanes
+    // come; inside: position < hi), four loads ahead
+    auto sweep = [&](int lo, int hi, auto f) {
+        for (int j0 = lo; j0 < hi; j0 += 128) {
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = j0 + 32 * k + lane < hi ? at(j0 + 32 * k + lane) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (j0 + 32 * k < hi) f(j0 + 32 * k + lane, key_of(x[k]));
+        }
+    };
 
     // ---- the last kept position in the order of sums: its key and position
     // (kept: larger keys, and the same key up to that position), and how many
@@ -101,7 +113,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
             for (int b = tid; b < nb; b += kSelThreads) bins[b] = 0;
             __syncthreads();
             if (pass == 0) {
-                constexpr int kAtOnce = kSelThreads == 1024 ? 8 : 4;
+                constexpr int kAtOnce = 4;
                 for (int j0 = tid; j0 < ctx; j0 += kAtOnce * kSelThreads) {
                     float x[kAtOnce];
 #pragma unroll
@@ -167,15 +179,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
             // each counts the ones before it
             unsigned long long *list = reinterpret_cast<unsigned long long *>(bins);
             uint32_t above = 0;
-            for (int j0 = lo; j0 < hi; j0 += 32) {
-                const int j = j0 + lane;
-                const uint32_t key = j < hi ? key_of(at(j)) : 0u;
-                const bool in = j < hi && (key & mask) == prefix;
+            sweep(lo, hi, [&](int j, uint32_t key) {
                 above += j < hi && (key & mask) > prefix;
-                if (in) {
+                if (j < hi && (key & mask) == prefix)
                     list[atomicAdd(&found[3], 1u)] = (unsigned long long)key << 32 | ~(uint32_t)j;
-                }
-            }
+            });
             __syncthreads();
             for (uint32_t i = tid; i < many; i += kSelThreads) {
                 const unsigned long long mine = list[i];
@@ -199,12 +207,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
         } else {
             // a key that many positions share: the want-th of them in order
             last = prefix;
-            for (int j0 = lo; j0 < hi; j0 += 32) {
-                const int j = j0 + lane;
-                const uint32_t key = j < hi ? key_of(at(j)) : 0u;
+            sweep(lo, hi, [&](int j, uint32_t key) {
                 more += __popc(__ballot_sync(kAll, j < hi && key > last));
                 same += __popc(__ballot_sync(kAll, j < hi && key == last));
-            }
+            });
             if (lane == 0) part2[warp] = same;
             __syncthreads();
             int ahead = 0;
@@ -234,9 +240,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     if (heavy > 0) {
         uint32_t out = 0;
         for (int k = 0; k < warp; ++k) out += part[k];
-        for (int j0 = lo; j0 < hi; j0 += 32) {
-            const int j = j0 + lane;
-            const uint32_t key = j < hi ? key_of(at(j)) : 0u;
+        sweep(lo, hi, [&](int j, uint32_t key) {
             const bool take = j < hi && (key > last || (key == last && j <= cut));
             const unsigned m = __ballot_sync(kAll, take);
             if (take) {
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
                 if (CACHED) wo[o] = row_sh[j];
             }
             out += __popc(m);
-        }
+        });
     }
     for (int j = tid; j < a.recent; j += kSelThreads) {
         keep[heavy + j] = old + j;
