@@ -162,9 +162,8 @@ __device__ __forceinline__ float4 unpack(const uint2 &r, T) {
     return make_float4(v[0], v[1], v[2], v[3]);
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -213,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const Ve
         }
         return;
     }
+    cluster_arrive();      // waited for before the first store to another CTA: it has started
     const T *P = static_cast<const T *>(a.p) + (size_t)row0 * V;
     const T *Q = DRAFT ? static_cast<const T *>(a.q) + (size_t)row0 * V : nullptr;
     const float us = a.u_sample[s];
@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const Ve
     // all warps add up that row, warp 0 goes on.
     int i = 1, cur = 0, k = 0, len = 1;
     bool pending = false;       // the last rejection's sum is not known yet
+    bool started = false;       // every CTA of the cluster has
     Pair z = {1.f, 0.f};
     int32_t *path = a.path + (size_t)s * a.max_q;
     const bool writer = rank == 0 && tid == 0;
@@ -388,10 +389,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const Ve
             if (lane == 0) sh.seg[warp][g] = sum;
             acc = add(acc, sum);
         }
+        if (!started) {
+            __syncwarp();
+            cluster_wait();
+            started = true;
+        }
         // to every CTA; two buffers, since a CTA of the cluster may still read the
         // last pass's (none can be two passes behind)
         if (lane < (int)C) store_cluster(&sh.sums[parity][gw], (uint32_t)lane, acc);
-        cluster_sync();
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
         if (warp == 0) {
             // lane l: the sums of warps kPerLane l .. of the row
             const Pair zero = {0.f, 0.f};
