@@ -644,8 +644,8 @@ int pa_evict_select(int32_t *keep, int32_t *keep_lens, float *weights_out, const
  *                 are not read
  *   keep_lens     [n_seqs] int32, <= keep_stride; <= 0 moves nothing
  * Reported in *status, the row (or, for a bad keep_lens or first, the sequence)
- * not moved: PA_ERR_INVALID_ARG for a keep entry that does not ascend or lies
- * outside the sequence, PA_ERR_BAD_BLOCK for a position past max_blocks * B or
+ * not moved: PA_ERR_INVALID_ARG for a keep entry that does not ascend, is less
+ * than its index (no ascending list has one) or lies outside the sequence, PA_ERR_BAD_BLOCK for a position past max_blocks * B or
  * a table entry outside the pool.  Any geometry of the device calls.
  * Errors: PA_ERR_INVALID_ARG, PA_ERR_CUDA. */
 int pa_compact_kv(void *const *k_caches, void *const *v_caches, int32_t num_layers,

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kv_kernel(const __grid_c
             if (j < len) {
                 const int at = keep[j], prev = j > 0 ? keep[j - 1] : -1;
                 const long long sp = (long long)first + at, dp = (long long)first + j;
-                if (at <= prev || at < 0 || sp >= ctx) {
+                if (at <= prev || at < j || sp >= ctx) {   // (at >= j: sources lie at or after their targets)
                     report(a.status, PA_ERR_INVALID_ARG);
                 } else if ((sp >> a.bshift) >= a.max_blocks) {
                     report(a.status, PA_ERR_BAD_BLOCK);
@@ -415,7 +415,7 @@ int launch_evict_select(int32_t *keep, int32_t *keep_lens, float *weights_out, c
     const dim3 grid((unsigned)num_heads, (unsigned)n_seqs);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    const int bytes = weight_len * 4;
+    const size_t bytes = (size_t)weight_len * 4;
     if (weight_len <= kShort) {
         evict_select_kernel<true, 256><<<grid, 256, bytes, st>>>(a);
     } else if (weight_len <= kCached) {

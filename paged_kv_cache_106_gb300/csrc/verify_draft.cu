@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const Ve
         }
         return;
     }
-    cluster_arrive();      // waited for before the first store to another CTA: it has started
+    cluster_arrive();      // waited for before the first store to another CTA: all have started then
     const T *P = static_cast<const T *>(a.p) + (size_t)row0 * V;
     const T *Q = DRAFT ? static_cast<const T *>(a.q) + (size_t)row0 * V : nullptr;
     const float us = a.u_sample[s];
@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const Ve
         sh.u[i] = a.u_accept[row0 + i];
     }
     __syncthreads();
+    cluster_wait();
 
     // Spans are counted from the vector boundary at or before the row's start.
     const int gw = (int)rank * kWarps + warp;          // this warp's place in the row
@@ -331,7 +332,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const Ve
     // all warps add up that row, warp 0 goes on.
     int i = 1, cur = 0, k = 0, len = 1;
     bool pending = false;       // the last rejection's sum is not known yet
-    bool started = false;       // every CTA of the cluster has
     Pair z = {1.f, 0.f};
     int32_t *path = a.path + (size_t)s * a.max_q;
     const bool writer = rank == 0 && tid == 0;
@@ -388,11 +388,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const Ve
             sum = over_lanes(sum);
             if (lane == 0) sh.seg[warp][g] = sum;
             acc = add(acc, sum);
-        }
-        if (!started) {
-            __syncwarp();
-            cluster_wait();
-            started = true;
         }
         // to every CTA; two buffers, since a CTA of the cluster may still read the
         // last pass's (none can be two passes behind)
