@@ -531,7 +531,9 @@ int pa_prefill_step_attention(void *out, const void *q, const void *k_new, const
  * 8, 16 or 32, n_seqs <= PA_TREE_MAX_SEQS.  How long contexts are cut into
  * parts depends on the whole batch, so a sequence's result agrees between
  * batches to rounding, not to the bit; it does not depend on where blocks are.
- * Slots past ctx are never used.  Reported in *status: PA_ERR_INVALID_ARG for
+ * Slots past ctx are never used, and what a row does not see never changes it,
+ * not where keys or values there are infinite or NaN (the head of that sequence
+ * then takes longer).  Reported in *status: PA_ERR_INVALID_ARG for
  * n < 0, n > ctx, n > max_q_len or rows outside [0, q_rows) (that sequence is
  * left unwritten), and for a parent that is no earlier node (taken as -1);
  * PA_ERR_BAD_BLOCK for ctx > max_blocks * B (left unwritten) or a table entry

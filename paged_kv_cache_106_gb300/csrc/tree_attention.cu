@@ -80,6 +80,7 @@ constexpr float kRescaleLog2 = 8.f;  // tensor-memory kernel: how far a row's ma
 struct TreeParams {
     __half *out;
     const __half *q;
+    const __half *k_cache, *v_cache;   // (read around the ring by plain_unit only)
     const int32_t *block_tables;
     const int32_t *ctx_lens;
     const int32_t *q_starts;   // NULL (weights form): one query a sequence
@@ -463,6 +464,63 @@ __device__ __forceinline__ int warp_combine(float (&v)[N], int lane, Op op) {
         }
     }
     return first;
+}
+
+// A unit's output rows once more without the matrix products, by the softmax
+// warps: where a node's value is not finite, 0 times it has put NaN into the
+// rows that do not see the node.  Here a row adds what it sees and nothing
+// else.  Thread = token, then dimension, as in the kernel; buf: NQ x kTile.
+// (Some 25 us a tile: for values that no working model has.)
+template <int D, int NQ>
+__device__ __noinline__ void plain_unit(const TreeParams &p, const int32_t *u, const uint64_t *seen,
+                                        const float *ref, float *buf, float *o) {
+    using Cfg = TreeCfg<D, NQ>;
+    constexpr int CQ = Cfg::CQ, ST = Cfg::SW * 32;
+    const int s = u[0], h = u[1], tok_first = u[4], n_tok = u[5], base = u[6], n = u[7], row0 = u[8];
+    const int H = p.num_heads, tok = threadIdx.x & 127, col0 = (threadIdx.x >> 7) * CQ;
+    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
+    // where the row of a position is in the caches, -1: in no block of the pool
+    auto at = [&](int pos) {
+        const int phys = table[pos >> p.bshift];
+        return phys < 0 || phys >= p.num_blocks
+                   ? -1ll
+                   : ((((long long)phys * H + h) << p.bshift) + (pos & ((1 << p.bshift) - 1))) * D;
+    };
+    auto rows_that_see = [&](int pos) { return (pos < base ? ~0ull : seen[pos - base]) >> col0; };
+    for (int i = 0; i < CQ; ++i) o[i] = 0.f;
+    for (int t0 = 0; t0 < n_tok; t0 += kTile) {
+        const int here = min(kTile, n_tok - t0);
+        const long long k_at = tok < here ? at(tok_first + t0 + tok) : -1;
+        const uint64_t who = k_at >= 0 ? rows_that_see(tok_first + t0 + tok) : 0;
+        for (int i = 0; i < CQ && col0 + i < n; ++i) {
+            float w = 0.f;
+            if ((who >> i) & 1) {
+                const __half2 *k = reinterpret_cast<const __half2 *>(p.k_cache + k_at);
+                const __half2 *q = reinterpret_cast<const __half2 *>(p.q + ((size_t)(row0 + col0 + i) * H + h) * D);
+                float x = 0.f;
+                for (int d = 0; d < D / 2; ++d) {
+                    const float2 a = __half22float2(k[d]), b = __half22float2(q[d]);
+                    x = fmaf(a.x, b.x, fmaf(a.y, b.y, x));
+                }
+                w = ex2(fmaf(x, p.qscale, -ref[col0 + i]));
+            }
+            buf[(col0 + i) * kTile + tok] = w;
+        }
+        softmax_sync<ST>();
+        if (tok < D)
+            for (int j = 0; j < here; ++j) {
+                const long long v_at = at(tok_first + t0 + j);
+                if (v_at < 0) continue;
+                const float v = __half2float(p.v_cache[v_at + tok]);
+                const uint64_t see = rows_that_see(tok_first + t0 + j);
+                for (int i = 0; i < CQ && col0 + i < n; ++i)
+                    if ((see >> i) & 1) o[i] = fmaf(buf[(col0 + i) * kTile + j], v, o[i]);
+            }
+        softmax_sync<ST>();
+    }
+    for (int i = threadIdx.x; i < NQ * kTile; i += ST) buf[i] = 0.f;   // (as P: finite)
+    fence_proxy_async_smem();
+    softmax_sync<ST>();
 }
 
 template <int D, int NQ, bool SCORES>
@@ -928,7 +986,8 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                 }
             }
             if (!softmax_all<ST>(ok)) break;
-            if (lane == 0) mbar_arrive(bar_unit_free + 8 * slot);
+            const bool nodes = !SCORES && knows && n > 1;    // some rows do not see all of the unit
+            if (lane == 0 && !nodes) mbar_arrive(bar_unit_free + 8 * slot);
             // sums over the tokens
             const int first = warp_combine(l, lane, [](float a, float c) { return a + c; });
 #pragma unroll
@@ -946,6 +1005,20 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
             tc::fence_after();
             float o[CQ];
             load_cols(Cfg::O_COL, o);
+            if (nodes) {
+                // (0 times a value that is not finite leaves no row's sum finite)
+                bool odd = tok < D && have > 0 && !isfinite(o[0]);
+                if (softmax_any<ST>(odd)) {
+#pragma unroll
+                    for (int i = 0; i < CQ; ++i) odd = odd && (i >= have || !isfinite(o[i]));
+                    float again[CQ];
+                    plain_unit<D, NQ>(p, u, seen + slot * 64, ref,
+                                      reinterpret_cast<float *>(tiles_at + stages * HALF), again);
+#pragma unroll
+                    for (int i = 0; i < CQ; ++i) o[i] = odd ? again[i] : o[i];
+                }
+                if (lane == 0) mbar_arrive(bar_unit_free + 8 * slot);
+            }
             if (tok < D) {                               // thread = dimension
                 if (parts == 1) {
                     __half *dst = p.out + ((size_t)(row0 + col0) * H + h) * D + tok;
@@ -1270,6 +1343,8 @@ int launch_common(const char *who, bool weights, TreeParams &p, const void *k_ca
     p.max_q = max_q;
     TreeMaps maps;
     const int64_t groups = (int64_t)d->num_blocks * d->num_heads * B / 8;
+    p.k_cache = static_cast<const __half *>(k_cache);
+    p.v_cache = static_cast<const __half *>(v_cache);
     int rc = encode_cache(&maps.k, k_cache, groups, d->head_dim, B / 8, who);
     if (rc == PA_OK) rc = encode_cache(&maps.v, v_cache, groups, d->head_dim, B / 8, who);
     if (rc == PA_OK) rc = encode_queries(&maps.q, p.q, p.q_rows, d->num_heads, d->head_dim, NR, who);
@@ -1326,7 +1401,7 @@ int launch_tree_attention(void *out, const void *q, const void *k_cache, const v
     if (mis(out, 16) || mis(q, 16) || mis(k_cache, 16) || mis(v_cache, 16) || mis(block_tables, 4) ||
         mis(ctx_lens, 4) || mis(q_starts, 4) || mis(parents, 4) || mis(status, 4))
         return fail(PA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
-    if (d->num_blocks < 1 || max_blocks < 1 || (int64_t)max_blocks * d->block_size > INT32_MAX)
+    if (d->num_blocks < 1 || max_blocks < 1 || (int64_t)max_blocks * d->block_size > INT32_MAX - kTile)
         return fail(PA_ERR_INVALID_ARG, "%s: num_blocks=%d, max_blocks=%d", who, d->num_blocks, max_blocks);
     TreeParams p{};
     p.out = static_cast<__half *>(out);
@@ -1370,7 +1445,7 @@ int launch_decode_attention_weights(void *out, float *weights_out, const float *
     if (mis(out, 16) || mis(q, 16) || mis(k_cache, 16) || mis(v_cache, 16) || mis(block_tables, 4) ||
         mis(ctx_lens, 4) || mis(weights_out, 4) || mis(weights_in, 4) || mis(status, 4))
         return fail(PA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
-    if (d->num_blocks < 1 || max_blocks < 1 || (int64_t)max_blocks * d->block_size > INT32_MAX)
+    if (d->num_blocks < 1 || max_blocks < 1 || (int64_t)max_blocks * d->block_size > INT32_MAX - kTile)
         return fail(PA_ERR_INVALID_ARG, "%s: num_blocks=%d, max_blocks=%d", who, d->num_blocks, max_blocks);
     const int64_t longest = std::min<int64_t>(weight_len, (int64_t)max_blocks * d->block_size);
     const dim3 grid(d->num_heads, n_seqs, (unsigned)std::max<int64_t>(1, (longest + kWeightChunk - 1) / kWeightChunk));
