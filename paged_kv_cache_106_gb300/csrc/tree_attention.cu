@@ -80,7 +80,7 @@ constexpr float kRescaleLog2 = 8.f;  // tensor-memory kernel: how far a row's ma
 struct TreeParams {
     __half *out;
     const __half *q;
-    const __half *k_cache, *v_cache;   // (read around the ring by plain_unit only)
+    const __half *k_cache, *v_cache;   // (read around the ring by node_tiles only)
     const int32_t *block_tables;
     const int32_t *ctx_lens;
     const int32_t *q_starts;   // NULL (weights form): one query a sequence
@@ -398,8 +398,8 @@ struct TreeCfg {
     static constexpr int SW = NQ == 16 ? 4 : 8, CQ = NQ / (SW / 4);
     static constexpr int PRODUCER = SW, PRODUCTS = SW + 1, Q_WARP = SW + 2;
     static constexpr int THREADS = (SW + 3) * 32;
-    // tensor-memory columns: two S, O (a power of two in all)
-    static constexpr uint32_t S_COL = 0, O_COL = 2 * NQ, COLS = 4 * NQ;
+    // tensor-memory columns: two S, O, O of the tiles that rows see different nodes of
+    static constexpr uint32_t S_COL = 0, O_COL = 2 * NQ, N_COL = 3 * NQ, COLS = 4 * NQ;
     static constexpr int BARS = 0;                           // full, empty; units; q, s, p, seen, o, done
     static constexpr int VARS = BARS + (2 * kMaxStages + 3 * kUnitSlots + 2 * 2 + 2 + 2 + 1 + 1) * 8;
     static constexpr int UNITS = (VARS + 16 + 15) / 16 * 16;
@@ -466,57 +466,84 @@ __device__ __forceinline__ int warp_combine(float (&v)[N], int lane, Op op) {
     return first;
 }
 
-// A unit's output rows once more without the matrix products, by the softmax
-// warps: where a node's value is not finite, 0 times it has put NaN into the
-// rows that do not see the node.  Here a row adds what it sees and nothing
-// else.  Thread = token, then dimension, as in the kernel; buf: NQ x kTile.
-// (Some 25 us a tile: for values that no working model has.)
+// The part of a unit's output that its tiles with nodes give, without the matrix
+// products, by the softmax warps: where a node's value is not finite,
+// 0 times it has put NaN into the rows that do not see the node.  Here a row
+// adds what it sees and nothing else, in the dimensions that are odd.  Thread =
+// token, then dimension, as in the kernel; buf: NQ x kTile.
+// Takes 0.1 ms a tile (64 rows), one or two tiles a unit: those tiles have an
+// accumulator of their own, so that the rest of a long unit needs no second
+// pass.  A look at every tile's values instead costs each unit without such
+// values: 256 sequences of 64 nodes took 820 us with it, 788 us so.
 template <int D, int NQ>
-__device__ __noinline__ void plain_unit(const TreeParams &p, const int32_t *u, const uint64_t *seen,
-                                        const float *ref, float *buf, float *o) {
+__device__ __noinline__ void node_tiles(const TreeParams &p, const int32_t *u, const uint64_t *seen,
+                                        const float *ref, float *buf, bool odd, float *o) {
     using Cfg = TreeCfg<D, NQ>;
     constexpr int CQ = Cfg::CQ, ST = Cfg::SW * 32;
     const int s = u[0], h = u[1], tok_first = u[4], n_tok = u[5], base = u[6], n = u[7], row0 = u[8];
-    const int H = p.num_heads, tok = threadIdx.x & 127, col0 = (threadIdx.x >> 7) * CQ;
+    const int H = p.num_heads, tok = threadIdx.x & 127, lane = threadIdx.x & 31, col0 = (threadIdx.x >> 7) * CQ;
     const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
-    // where the row of a position is in the caches, -1: in no block of the pool
+    // where a position's row is in the caches, -1: in no block of the pool
     auto at = [&](int pos) {
         const int phys = table[pos >> p.bshift];
         return phys < 0 || phys >= p.num_blocks
                    ? -1ll
                    : ((((long long)phys * H + h) << p.bshift) + (pos & ((1 << p.bshift) - 1))) * D;
     };
-    auto rows_that_see = [&](int pos) { return (pos < base ? ~0ull : seen[pos - base]) >> col0; };
-    for (int i = 0; i < CQ; ++i) o[i] = 0.f;
-    for (int t0 = 0; t0 < n_tok; t0 += kTile) {
+    auto rows_that_see = [&](int pos) { return (uint64_t)(pos < base ? ~0ull : seen[pos - base]) >> col0; };
+    float sum[CQ] = {};
+#pragma unroll 1
+    for (int t0 = max(0, base - tok_first) / kTile * kTile; t0 < n_tok; t0 += kTile) {
         const int here = min(kTile, n_tok - t0);
         const long long k_at = tok < here ? at(tok_first + t0 + tok) : -1;
         const uint64_t who = k_at >= 0 ? rows_that_see(tok_first + t0 + tok) : 0;
-        for (int i = 0; i < CQ && col0 + i < n; ++i) {
-            float w = 0.f;
-            if ((who >> i) & 1) {
-                const __half2 *k = reinterpret_cast<const __half2 *>(p.k_cache + k_at);
-                const __half2 *q = reinterpret_cast<const __half2 *>(p.q + ((size_t)(row0 + col0 + i) * H + h) * D);
-                float x = 0.f;
-                for (int d = 0; d < D / 2; ++d) {
-                    const float2 a = __half22float2(k[d]), b = __half22float2(q[d]);
-                    x = fmaf(a.x, b.x, fmaf(a.y, b.y, x));
+        // (64 dimensions at a time: no registers are left for more)
+#pragma unroll 1
+        for (int d0 = 0; d0 < D; d0 += 64) {
+            uint4 k[8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                k[d] = k_at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.k_cache + k_at + d0) + d) : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+            for (int i = 0; i < CQ && col0 + i < n; ++i) {
+                const uint4 *q = reinterpret_cast<const uint4 *>(p.q + ((size_t)(row0 + col0 + i) * H + h) * D + d0);
+                float *to = buf + (col0 + i) * kTile + tok, x = d0 ? *to : 0.f;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                    const uint4 q8 = __ldg(q + d);
+                    const uint32_t a[4] = {k[d].x, k[d].y, k[d].z, k[d].w}, b[4] = {q8.x, q8.y, q8.z, q8.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 fa = __half22float2(*reinterpret_cast<const __half2 *>(&a[e]));
+                        const float2 fb = __half22float2(*reinterpret_cast<const __half2 *>(&b[e]));
+                        x = fmaf(fa.x, fb.x, fmaf(fa.y, fb.y, x));
+                    }
                 }
-                w = ex2(fmaf(x, p.qscale, -ref[col0 + i]));
+                if (d0 + 64 == D) x = (who >> i) & 1 ? ex2(fmaf(x, p.qscale, -ref[col0 + i])) : 0.f;
+                *to = x;
             }
-            buf[(col0 + i) * kTile + tok] = w;
         }
         softmax_sync<ST>();
-        if (tok < D)
-            for (int j = 0; j < here; ++j) {
-                const long long v_at = at(tok_first + t0 + j);
-                if (v_at < 0) continue;
-                const float v = __half2float(p.v_cache[v_at + tok]);
-                const uint64_t see = rows_that_see(tok_first + t0 + j);
-                for (int i = 0; i < CQ && col0 + i < n; ++i)
-                    if ((see >> i) & 1) o[i] = fmaf(buf[(col0 + i) * kTile + j], v, o[i]);
+        if (__any_sync(kAll, odd))
+            for (int j0 = 0; j0 < here; j0 += 32) {
+                // a token a lane: where it is, and who sees it
+                const long long mine = j0 + lane < here ? at(tok_first + t0 + j0 + lane) : -1;
+                const uint64_t see = mine >= 0 ? rows_that_see(tok_first + t0 + j0 + lane) : 0;
+#pragma unroll 4
+                for (int j = 0; j < 32; ++j) {
+                    const long long v_at = __shfl_sync(kAll, mine, j);
+                    const uint64_t by = __shfl_sync(kAll, see, j);
+                    const float v = odd && v_at >= 0 ? __half2float(p.v_cache[v_at + tok]) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < CQ; ++i)
+                        if ((by >> i) & 1) sum[i] = fmaf(buf[(col0 + i) * kTile + j0 + j], v, sum[i]);
+                }
             }
         softmax_sync<ST>();
+    }
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < CQ; ++i) o[i] = sum[i];
     }
     for (int i = threadIdx.x; i < NQ * kTile; i += ST) buf[i] = 0.f;   // (as P: finite)
     fence_proxy_async_smem();
@@ -586,6 +613,11 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
     tc::fence_after();
     const uint32_t tmem = (uint32_t)vars[2];
     const int n_ord = vars[0], n_units = pre[n_ord] * H;
+    // First tile of a slot's unit that rows may see different nodes of; INT_MAX: none.
+    auto first_node_tile = [&](int slot) {
+        const int32_t *u = units + slot * 16;
+        return !SCORES && u[7] > 1 && u[4] + u[5] > u[6] ? max(0, u[6] - u[4]) / kTile : INT_MAX;
+    };
     bool ok = true;
 
     if (warp == Cfg::PRODUCER) {
@@ -774,7 +806,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
             for (uint32_t k = 0;; ++k) {
                 const int slot = k % kUnitSlots;
                 if (!wait(bar_unit + 8 * slot, (k / kUnitSlots) & 1u)) break;
-                const int n_tiles = (units[slot * 16 + 5] + kTile - 1) / kTile;
+                const int n_tiles = (units[slot * 16 + 5] + kTile - 1) / kTile, node_tile = first_node_tile(slot);
                 mbar_arrive(bar_unit_free + 8 * slot);
                 if (n_tiles == 0) break;
                 q_buf = k % QB;
@@ -793,8 +825,8 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                     const uint64_t dp = tc::smem_desc(sP + (gp & 1) * Cfg::P_BYTES, 1024, 1024);
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_ss(tmem + Cfg::O_COL, dv + ((kk * 2048u * NP) >> 4), dp + ((kk * 2048u) >> 4), idO,
-                                   (t > 0 || kk > 0) ? 1u : 0u);
+                        tc::mma_ss(tmem + (t < node_tile ? Cfg::O_COL : Cfg::N_COL), dv + ((kk * 2048u * NP) >> 4),
+                                   dp + ((kk * 2048u) >> 4), idO, ((t > 0 && t != node_tile) || kk > 0) ? 1u : 0u);
                     tc::commit(bar_empty + 8 * st_v);
                     if (t + 1 == n_tiles) tc::commit(bar_o);
                     ++gp;
@@ -839,6 +871,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                       n = u[7], row0 = u[8];
             if (n_tok <= 0) break;                       // the end
             const int have = n - col0;                   // rows of this thread's that exist
+            const int node_tile = first_node_tile(slot);
             bool knows = false;                          // who sees the nodes is there
             float l[R], off[R];                          // running sums; minus the rows' references
 #pragma unroll
@@ -916,16 +949,19 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                         const int st_o = st_v >= 2 ? st_v - 2 : st_v - 2 + stages;
                         wait(bar_empty + 8 * st_o, (st_v >= 2 ? use_v : use_v - 1) & 1u);
                         tc::fence_after();
-                        float o[CQ];
-                        load_cols(Cfg::O_COL, o);
+#pragma unroll 1
+                        for (int half = node_tile == 0; half <= (t0 > node_tile * (int64_t)kTile); ++half) {
+                            float o[CQ];
+                            load_cols(Cfg::O_COL + half * NQ, o);
 #pragma unroll
-                        for (int i = 0; i < R; ++i) o[i] *= corr[col0 + i];
-                        uint32_t r[CQ];
+                            for (int i = 0; i < R; ++i) o[i] *= corr[col0 + i];
+                            uint32_t r[CQ];
 #pragma unroll
-                        for (int i = 0; i < CQ; ++i) r[i] = __float_as_uint(o[i]);
-                        __syncwarp();
-                        if constexpr (CQ == 16) tc::st16(lane_base + Cfg::O_COL + col0, r);
-                        else tc::st32(lane_base + Cfg::O_COL + col0, r);
+                            for (int i = 0; i < CQ; ++i) r[i] = __float_as_uint(o[i]);
+                            __syncwarp();
+                            if constexpr (CQ == 16) tc::st16(lane_base + Cfg::O_COL + half * NQ + col0, r);
+                            else tc::st32(lane_base + Cfg::O_COL + half * NQ + col0, r);
+                        }
                         tc::wait_st();
                     }
                     scores();
@@ -986,7 +1022,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                 }
             }
             if (!softmax_all<ST>(ok)) break;
-            const bool nodes = !SCORES && knows && n > 1;    // some rows do not see all of the unit
+            const bool nodes = node_tile != INT_MAX;
             if (lane == 0 && !nodes) mbar_arrive(bar_unit_free + 8 * slot);
             // sums over the tokens
             const int first = warp_combine(l, lane, [](float a, float c) { return a + c; });
@@ -1004,20 +1040,31 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
             wait(bar_o, k & 1u);
             tc::fence_after();
             float o[CQ];
-            load_cols(Cfg::O_COL, o);
-            if (nodes) {
+            if (!nodes) {
+                load_cols(Cfg::O_COL, o);
+            } else {
+                load_cols(Cfg::N_COL, o);
                 // (0 times a value that is not finite leaves no row's sum finite)
                 bool odd = tok < D && have > 0 && !isfinite(o[0]);
-                if (softmax_any<ST>(odd)) {
+                const bool some = softmax_any<ST>(odd);
+                if (some) {
 #pragma unroll
                     for (int i = 0; i < CQ; ++i) odd = odd && (i >= have || !isfinite(o[i]));
                     float again[CQ];
-                    plain_unit<D, NQ>(p, u, seen + slot * 64, ref,
-                                      reinterpret_cast<float *>(tiles_at + stages * HALF), again);
 #pragma unroll
-                    for (int i = 0; i < CQ; ++i) o[i] = odd ? again[i] : o[i];
+                    for (int i = 0; i < CQ; ++i) again[i] = o[i];
+                    node_tiles<D, NQ>(p, u, seen + slot * 64, ref,
+                                      reinterpret_cast<float *>(tiles_at + stages * HALF), odd, again);
+#pragma unroll
+                    for (int i = 0; i < CQ; ++i) o[i] = again[i];
                 }
                 if (lane == 0) mbar_arrive(bar_unit_free + 8 * slot);
+                if (node_tile > 0) {
+                    float before[CQ];
+                    load_cols(Cfg::O_COL, before);
+#pragma unroll
+                    for (int i = 0; i < CQ; ++i) o[i] += before[i];
+                }
             }
             if (tok < D) {                               // thread = dimension
                 if (parts == 1) {
