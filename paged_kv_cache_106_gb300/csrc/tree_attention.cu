@@ -135,6 +135,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// One lane of a warp whose lanes are all here, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // Lets the kernel launched after this one start (it then waits, at
 // wait_for_launch_before, for this one's end).
 __device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -573,7 +580,8 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
     uint16_t *order = reinterpret_cast<uint16_t *>(len + S);
     uint8_t *tiles_at = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(order + S) + 1023) & ~uintptr_t(1023));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the shuffles here and in the products' warp tell the compiler that a warp's lanes agree)
+    const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
     const int stages = p.stages, bshift = p.bshift, B = 1 << bshift, bps = kTile >> bshift;
     // (for D = 64 the second half of V^T's rows is whatever lies 1 KB on: the
     // ring is followed by P)
@@ -767,73 +775,81 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
             mbar_wait_bounded(bar_q + 8 * (i % QB), (i / QB) & 1u, p.status, false);
         __syncwarp();
     } else if (warp == Cfg::PRODUCTS) {
-        // ================================================ products, one thread
+        // ================================================ products
         // Order: S of tile t + 1 before O of tile t, so that the softmax of a
-        // tile finds its S ready; S and P have two buffers, taken in turn.
-        if (lane == 0) {
-            constexpr uint32_t idS = tc::idesc_f16(kTile, NQ, false);
-            constexpr uint32_t idO = tc::idesc_f16(128, NQ, true) | (1u << 15);   // both MN-major
-            int st = 0, st_v = 1;        // stage of the next keys; of the next values
-            uint32_t use = 0, use_v = 0, gs = 0, gp = 0;   // tiles whose S, whose O was issued
-            uint32_t q_buf = 0;
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                ok = ok && mbar_wait_bounded(bar, parity, p.status, true);
-                return ok;
-            };
-            auto step = [&](int &i, uint32_t &n) {
-                i += 2;
-                if (i >= stages) {
-                    i -= stages;
-                    ++n;
-                }
-            };
-            // S (tokens x rows) = K Q^T
-            auto issue_s = [&]() {
-                if (!wait(bar_full + 8 * st, use & 1u)) return;
-                tc::fence_after();
-                const uint64_t dk = tc::smem_desc(ring + st * HALF, 16, 1024u * NP);
-                const uint64_t dq = tc::smem_desc(sQ + q_buf * Cfg::Q_BYTES, 16, 1024);
+        // tile finds its S ready; S and P have two buffers, taken in turn.  The
+        // warp goes along together and one lane issues: its operands then lie
+        // in uniform registers.  (With one lane going alone a product took 100
+        // clocks to issue, so 60 to 75.)
+        constexpr uint32_t idS = tc::idesc_f16(kTile, NQ, false);
+        constexpr uint32_t idO = tc::idesc_f16(128, NQ, true) | (1u << 15);   // both MN-major
+        int st = 0, st_v = 1;            // stage of the next keys; of the next values
+        uint32_t use = 0, use_v = 0, gs = 0, gp = 0;   // tiles whose S, whose O was issued
+        uint32_t q_buf = 0;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(kAll, ok && mbar_wait_bounded(bar, parity, p.status, true));
+            return ok;
+        };
+        auto step = [&](int &i, uint32_t &n) {
+            i += 2;
+            if (i >= stages) {
+                i -= stages;
+                ++n;
+            }
+        };
+        // S (tokens x rows) = K Q^T; the unit's last: Q is not needed any more
+        auto issue_s = [&](bool last) {
+            if (!wait(bar_full + 8 * st, use & 1u)) return;
+            tc::fence_after();
+            const uint64_t dk = tc::smem_desc(ring + st * HALF, 16, 1024u * NP);
+            const uint64_t dq = tc::smem_desc(sQ + q_buf * Cfg::Q_BYTES, 16, 1024);
+            const uint32_t d = tmem + Cfg::S_COL + (gs & 1) * NQ;
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    tc::mma_ss(tmem + Cfg::S_COL + (gs & 1) * NQ,
-                               dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                    tc::mma_ss(d, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
                                dq + (((kk >> 2) * NQ * 128 + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
                 tc::commit(bar_empty + 8 * st);
                 tc::commit(bar_s + 8 * (gs & 1));
-                ++gs;
-                step(st, use);
-            };
-            for (uint32_t k = 0;; ++k) {
-                const int slot = k % kUnitSlots;
-                if (!wait(bar_unit + 8 * slot, (k / kUnitSlots) & 1u)) break;
-                const int n_tiles = (units[slot * 16 + 5] + kTile - 1) / kTile, node_tile = first_node_tile(slot);
-                mbar_arrive(bar_unit_free + 8 * slot);
-                if (n_tiles == 0) break;
-                q_buf = k % QB;
-                if (!wait(bar_q + 8 * q_buf, (k / QB) & 1u)) break;
-                issue_s();
-                if (n_tiles == 1) tc::commit(bar_q_free + 8 * q_buf);
-                for (int t = 0; ok && t < n_tiles; ++t) {
-                    if (t + 1 < n_tiles) {
-                        issue_s();
-                        if (t + 2 == n_tiles) tc::commit(bar_q_free + 8 * q_buf);
-                    }
-                    if (!wait(bar_full + 8 * st_v, use_v & 1u) || !wait(bar_p + 8 * (gp & 1), (gp >> 1) & 1u)) break;
-                    tc::fence_after();
-                    // O (dims x rows) += V^T P^T
-                    const uint64_t dv = tc::smem_desc(ring + st_v * HALF, 1024, 1024u * NP);
-                    const uint64_t dp = tc::smem_desc(sP + (gp & 1) * Cfg::P_BYTES, 1024, 1024);
+                if (last) tc::commit(bar_q_free + 8 * q_buf);
+            }
+            __syncwarp();
+            ++gs;
+            step(st, use);
+        };
+        for (uint32_t k = 0;; ++k) {
+            const int slot = k % kUnitSlots;
+            if (!wait(bar_unit + 8 * slot, (k / kUnitSlots) & 1u)) break;
+            const int n_tiles = __shfl_sync(kAll, (units[slot * 16 + 5] + kTile - 1) / kTile, 0);
+            const int node_tile = __shfl_sync(kAll, first_node_tile(slot), 0);
+            if (lane == 0) mbar_arrive(bar_unit_free + 8 * slot);
+            if (n_tiles == 0) break;
+            q_buf = k % QB;
+            if (!wait(bar_q + 8 * q_buf, (k / QB) & 1u)) break;
+            issue_s(n_tiles == 1);
+            for (int t = 0; ok && t < n_tiles; ++t) {
+                if (t + 1 < n_tiles) issue_s(t + 2 == n_tiles);
+                if (!wait(bar_full + 8 * st_v, use_v & 1u) || !wait(bar_p + 8 * (gp & 1), (gp >> 1) & 1u)) break;
+                tc::fence_after();
+                // O (dims x rows) += V^T P^T
+                const uint64_t dv = tc::smem_desc(ring + st_v * HALF, 1024, 1024u * NP);
+                const uint64_t dp = tc::smem_desc(sP + (gp & 1) * Cfg::P_BYTES, 1024, 1024);
+                const uint32_t d = tmem + (t < node_tile ? Cfg::O_COL : Cfg::N_COL);
+                const uint32_t more = t > 0 && t != node_tile ? 1u : 0u;
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_ss(tmem + (t < node_tile ? Cfg::O_COL : Cfg::N_COL), dv + ((kk * 2048u * NP) >> 4),
-                                   dp + ((kk * 2048u) >> 4), idO, ((t > 0 && t != node_tile) || kk > 0) ? 1u : 0u);
+                        tc::mma_ss(d, dv + ((kk * 2048u * NP) >> 4), dp + ((kk * 2048u) >> 4), idO, kk > 0 ? 1u : more);
                     tc::commit(bar_empty + 8 * st_v);
                     if (t + 1 == n_tiles) tc::commit(bar_o);
-                    ++gp;
-                    step(st_v, use_v);
                 }
-                if (!ok) break;
+                __syncwarp();
+                ++gp;
+                step(st_v, use_v);
             }
+            if (!ok) break;
+        }
+        if (elect_one()) {
             if (!ok) report(p.status, PA_ERR_TIMEOUT);
             tc::commit(bar_done);   // lets the teardown wait for every product issued
         }
