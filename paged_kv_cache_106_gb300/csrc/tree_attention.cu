@@ -187,24 +187,54 @@ __device__ __forceinline__ int warp_incl_scan(int v, int lane) {
     return v;
 }
 
-// How many tiles a part may have.  A unit costs its tiles, about one more to
-// get going, and where it is a part of a cut sequence the writing and joining
-// of its rows.  Every lane brings a candidate: the longest sequence in
-// lane + 1 parts, and how many units (before heads) and parts that makes.
-__device__ __forceinline__ int part_size(const TreeParams &p, long long total, int longest, int some, int HG,
-                                         int mine, int units_n, int cuts, int lane) {
-    const int slots = gridDim.x, extra = kTile + 2 * p.max_q;     // in tokens
+// A lane's candidate for how many tiles a part may have, and what comes of it.
+struct Cuts {
+    int size;          // tiles of a part, at most
+    int units, parts;  // units of all sequences; of them parts of cut ones
+    int tiles;         // of the cut ones
+    __device__ void take(int l) {
+        const int n = (l + size - 1) / size;
+        units += n;
+        if (n > 1) {
+            parts += n;
+            tiles += l;
+        }
+    }
+};
+// The longest sequence in lane + 1 parts.  (More would serve a long context of
+// one head and hurt where rows to join are many: with up to 125 parts, 70000
+// positions and 8 rows 29.0 us instead of 31.0, 2 heads' 2 x 30000 and 64 rows
+// 29.4 us instead of 27.9.)
+__device__ __forceinline__ Cuts candidate(int longest, int lane) {
+    return {max(1, (longest + lane) / (lane + 1)), 0, 0, 0};
+}
+
+// How many tiles a part may have: the candidate with the earliest end.  A unit
+// costs its tiles, about one more to get going, and where it is a part of a cut
+// sequence the writing and joining of its rows.  The last CTA is done when all
+// work would be, evenly shared; or after as many parts as it must take (they
+// are alike: 1056 units on 152 CTAs are 7 each, 1440 are 10 where 9.5 would be
+// even), or, where whole sequences come last, half one of these late.  (Over
+// random batches the choice ends 3 % after the best candidate's end; half a part
+// late for every cut ended 5 % after it: 3 sequences of 60000 at 32 heads 241 us
+// instead of 232, 2 at 40 heads 393 instead of 386.)
+__device__ __forceinline__ int part_size(const TreeParams &p, long long total, int some, int HG, const Cuts &c,
+                                         int lane) {
+    const int slots = gridDim.x;
     // many units: parts of a quarter of an SM's share
     if ((long long)some * HG >= 4 * slots) return max(1, (int)((total * HG + 4 * slots - 1) / (4 * slots)));
-    // few: by what the last SM would be done at
-    const float units_all = (float)units_n * HG;
-    const float all = ((float)total * HG * kTile + units_all * (lane ? extra : kTile)) / slots;
-    float end = fmaxf(units_all > slots ? all + 0.5f * mine * kTile : all, (float)mine * kTile + extra);
-    if (cuts > p.cap) end = INFINITY;
+    const float extra = lane ? 1.f + p.max_q * (2.f / kTile) : 1.f;   // in tiles
+    const float all = ((float)total * HG + (float)c.units * HG * extra) / slots;
+    float end = fmaxf(all, (float)c.size + extra);
+    if (c.parts > 0)
+        end = fmaxf(end, (float)((c.parts * HG + slots - 1) / slots) * ((float)c.tiles / c.parts + extra));
+    if (c.units > c.parts && c.units * HG > slots)
+        end = fmaxf(end, all + 0.5f * (float)(total - c.tiles) / (c.units - c.parts));
+    if (c.parts > p.cap) end = INFINITY;
     float best = end;
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) best = fminf(best, __shfl_xor_sync(kAll, best, off));
-    return __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, end == best)) - 1);
+    return __shfl_sync(kAll, c.size, __ffs(__ballot_sync(kAll, end == best)) - 1);
 }
 
 // The launch's work plan, the same in every CTA, by all its threads: len[s]
@@ -227,14 +257,9 @@ __device__ void make_plan(const TreeParams &p, int32_t *pre, int32_t *len, uint1
         const int l = lane < S ? len[lane] : 0;
         const int total = __reduce_add_sync(kAll, l), longest = __reduce_max_sync(kAll, l);
         const int some = __popc(__ballot_sync(kAll, l > 0));
-        const int mine = max(1, (longest + lane) / (lane + 1));
-        int units_n = 0, cuts = 0;
-        for (int s = 0; s < S; ++s) {
-            const int parts = (__shfl_sync(kAll, l, s) + mine - 1) / mine;
-            units_n += parts;
-            cuts += parts > 1 ? parts : 0;
-        }
-        const int P = part_size(p, total, longest, some, HG, mine, units_n, cuts, lane);
+        Cuts c = candidate(longest, lane);
+        for (int s = 0; s < S; ++s) c.take(__shfl_sync(kAll, l, s));
+        const int P = part_size(p, total, some, HG, c, lane);
         const int parts = (l + P - 1) / P, key = parts > 1 ? INT_MAX : l;
         int rank = 0;
         for (int s = 0; s < S; ++s) {
@@ -269,15 +294,11 @@ __device__ void make_plan(const TreeParams &p, int32_t *pre, int32_t *len, uint1
             some += __shfl_xor_sync(kAll, some, off);
             longest = max(longest, __shfl_xor_sync(kAll, longest, off));
         }
-        const int mine = max(1, (longest + lane) / (lane + 1));
-        int units_n = 0, cuts = 0, cut_parts;
+        int cut_parts;
+        Cuts c = candidate(longest, lane);
         if ((long long)some * HG < 4 * (int)gridDim.x)
-            for (int s = 0; s < S; ++s) {
-                const int n = (len[s] + mine - 1) / mine;
-                units_n += n;
-                cuts += n > 1 ? n : 0;
-            }
-        int P = part_size(p, total, longest, some, HG, mine, units_n, cuts, lane);
+            for (int s = 0; s < S; ++s) c.take(len[s]);
+        int P = part_size(p, total, some, HG, c, lane);
         while (true) {   // (more than the cap only where the first case found none)
             cut_parts = 0;
             for (int s = lo_s; s < hi_s; ++s)
