@@ -678,8 +678,10 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
             u.s = order[lo];
             u.parts = pre[lo + 1] - pre[lo];
             const int part = u.gp - pre[lo], l = len[u.s];
-            u.b0 = (int)((long long)part * l / u.parts) * bps;
-            u.nb = (int)((long long)(part + 1) * l / u.parts) * bps - u.b0;
+            // even parts, the first ones a tile longer
+            const int even = l / u.parts, more = l - even * u.parts;
+            u.b0 = (part * even + min(part, more)) * bps;
+            u.nb = (even + (part < more)) * bps;
             // (the sequence's last blocks may be fewer)
             if (u.b0 + lane < p.max_blocks && lane < u.nb)
                 u.tbl = p.block_tables[(size_t)u.s * p.max_blocks + u.b0 + lane];
@@ -1001,7 +1003,15 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                         }
                         tc::wait_st();
                     }
-                    scores();
+                    // (32 rows a thread do not stay in registers up to here: spilled
+                    // they cost more than the second load, 785 instead of 771 us
+                    // for 256 sequences of 64 nodes)
+                    if constexpr (R <= 16) {
+#pragma unroll
+                        for (int i = 0; i < R; ++i) y[i] += off[i];
+                    } else {
+                        scores();
+                    }
                 }
                 // P of the tile: this token's row, in the second operand's layout
                 uint32_t w[(R + 7) / 8 * 4];
