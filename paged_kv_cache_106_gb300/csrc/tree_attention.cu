@@ -209,7 +209,9 @@ __device__ __forceinline__ Cuts candidate(int longest, int lane) {
     return {max(1, (longest + lane) / (lane + 1)), 0, 0, 0};
 }
 
-// How many tiles a part may have: the candidate with the earliest end.  A unit
+// How many tiles a part may have: the candidate with the earliest end.  (Its
+// parts fit the workspace: lane 0 cuts nothing, and parts of a quarter of an SM's
+// share are at most two for each such quarter in a cut sequence.)  A unit
 // costs its tiles, about one more to get going, and where it is a part of a cut
 // sequence the writing and joining of its rows.  The last CTA is done when all
 // work would be, evenly shared; or after as many parts as it must take (they
@@ -237,6 +239,113 @@ __device__ __forceinline__ int part_size(const TreeParams &p, long long total, i
     return __shfl_sync(kAll, c.size, __ffs(__ballot_sync(kAll, end == best)) - 1);
 }
 
+// What the plan of more than 32 sequences adds up over the warps.
+struct PlanSums {
+    unsigned long long total;          // tiles
+    int some, longest;                 // sequences with work, tiles of the longest
+    int units[32], parts[32], tiles[32];   // by candidate
+};
+
+// More than 32 sequences: by all warps, in chunks of 32.  (A function of its own:
+// its instructions are not in the way of small batches.)
+template <bool SCORES>
+__device__ __noinline__ void plan_of_many(const TreeParams &p, int32_t *pre, int32_t *len, uint16_t *order,
+                                          int32_t *vars, int32_t *counts, int HG) {
+    const int S = p.n_seqs, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n_warps = blockDim.x >> 5;
+    PlanSums *sums = reinterpret_cast<PlanSums *>(counts);
+    for (int i = tid; i < (int)(sizeof(PlanSums) / 4); i += (int)blockDim.x) counts[i] = 0;
+    __syncthreads();
+    for (int s0 = warp * 32; s0 < S; s0 += (int)blockDim.x) {
+        const int s = s0 + lane;
+        int l = 0;
+        if (s < S) {
+            const SeqRows r = rows_of<SCORES>(p, s, blockIdx.x == 0);
+            len[s] = l = r.n > 0 ? (r.ctx + kTile - 1) / kTile : 0;
+        }
+        const int add = __reduce_add_sync(kAll, l), top = __reduce_max_sync(kAll, l);
+        const int n = __popc(__ballot_sync(kAll, l > 0));
+        if (lane == 0) {
+            atomicAdd(&sums->total, (unsigned long long)add);
+            atomicMax(&sums->longest, top);
+            atomicAdd(&sums->some, n);
+        }
+    }
+    __syncthreads();
+    const int chunks = (S + 31) / 32, some = sums->some, longest = sums->longest;
+    const long long total = (long long)sums->total;
+    Cuts c = candidate(longest, lane);
+    if ((long long)some * HG < 4 * (int)gridDim.x) {
+        for (int s = warp; s < S; s += n_warps) c.take(len[s]);
+        atomicAdd(&sums->units[lane], c.units);
+        atomicAdd(&sums->parts[lane], c.parts);
+        atomicAdd(&sums->tiles[lane], c.tiles);
+        __syncthreads();
+        c.units = sums->units[lane];
+        c.parts = sums->parts[lane];
+        c.tiles = sums->tiles[lane];
+    }
+    const int P = part_size(p, total, some, HG, c, lane);
+    // counting sort by size class: 0 the cut ones, 1 .. 31 the others, long
+    // ones first, in order of index within a class; 32: no work
+    int32_t *at = counts + sizeof(PlanSums) / 4;     // [chunk][33]
+    const int top = max(1, min(P, longest));
+    auto cls = [&](int s) {
+        const int l = s < S ? len[s] : 0;
+        return l == 0 ? 32 : l > P ? 0 : 1 + (top - l) * 30 / top;   // (below 2^24 tiles)
+    };
+    auto rank = [&](int k, unsigned &same) {
+        same = __match_any_sync(kAll, k);
+        return __popc(same & ((1u << lane) - 1));
+    };
+    unsigned same;
+    for (int ch = warp; ch < chunks; ch += n_warps) {
+        at[ch * 33 + lane] = 0;
+        __syncwarp();
+        const int k = cls(ch * 32 + lane), r = rank(k, same);
+        if (r == 0 && k < 32) at[ch * 33 + k] = __popc(same);
+    }
+    __syncthreads();
+    if (warp == 0) {                 // lane = class: where its chunks' sequences start
+        int mine = 0;
+        for (int ch = 0; ch < chunks; ++ch) mine += at[ch * 33 + lane];
+        const int incl = warp_incl_scan(mine, lane);
+        int run = incl - mine;
+        for (int ch = 0; ch < chunks; ++ch) {
+            const int n = at[ch * 33 + lane];
+            at[ch * 33 + lane] = run;
+            run += n;
+        }
+        if (lane == 31) vars[0] = incl;
+        if (lane == 0) vars[1] = incl;
+    }
+    __syncthreads();
+    for (int ch = warp; ch < chunks; ch += n_warps) {
+        const int k = cls(ch * 32 + lane), r = rank(k, same);
+        if (k < 32) order[at[ch * 33 + k] + r] = (uint16_t)(ch * 32 + lane);
+    }
+    __syncthreads();
+    // running sums of the parts in that order: within chunks, then of chunks
+    const int n_ord = vars[0];
+    for (int ch = warp; ch * 32 < n_ord; ch += n_warps) {
+        const int i = ch * 32 + lane, parts = i < n_ord ? (len[order[i]] + P - 1) / P : 0;
+        const int incl = warp_incl_scan(parts, lane);
+        if (i < n_ord) pre[i] = incl - parts;
+        if (lane == 31) at[ch] = incl;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int base = 0;
+        for (int c0 = 0; c0 * 32 < n_ord; c0 += 32) {
+            const int n = (c0 + lane) * 32 < n_ord ? at[c0 + lane] : 0, incl = warp_incl_scan(n, lane);
+            if ((c0 + lane) * 32 < n_ord) at[c0 + lane] = base + incl - n;
+            base += __shfl_sync(kAll, incl, 31);
+        }
+        if (lane == 0) pre[n_ord] = base;
+    }
+    __syncthreads();
+    for (int i = tid; i < n_ord; i += (int)blockDim.x) pre[i] += at[i >> 5];
+}
+
 // The launch's work plan, the same in every CTA, by all its threads: len[s]
 // tiles of sequence s (0: no work), order[] the sequences with work, pre[i]
 // the parts of those before the i-th; vars: how many have work, how many of
@@ -247,14 +356,16 @@ template <bool SCORES>
 __device__ void make_plan(const TreeParams &p, int32_t *pre, int32_t *len, uint16_t *order, int32_t *vars,
                           int32_t *counts, int HG) {
     const int S = p.n_seqs, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int s = tid; s < S; s += (int)blockDim.x) {
-        const SeqRows r = rows_of<SCORES>(p, s, blockIdx.x == 0);
-        len[s] = r.n > 0 ? (r.ctx + kTile - 1) / kTile : 0;
-    }
-    __syncthreads();
-    if (warp == 0 && S <= 32) {
-        // a sequence a lane: the plan below without its loops
-        const int l = lane < S ? len[lane] : 0;
+    if (S > 32) {
+        plan_of_many<SCORES>(p, pre, len, order, vars, counts, HG);
+    } else if (warp == 0) {
+        // a sequence a lane: the same without loops
+        int l = 0;
+        if (lane < S) {
+            const SeqRows r = rows_of<SCORES>(p, lane, blockIdx.x == 0);
+            len[lane] = l = r.n > 0 ? (r.ctx + kTile - 1) / kTile : 0;
+        }
+        __syncwarp();
         const int total = __reduce_add_sync(kAll, l), longest = __reduce_max_sync(kAll, l);
         const int some = __popc(__ballot_sync(kAll, l > 0));
         Cuts c = candidate(longest, lane);
@@ -277,70 +388,6 @@ __device__ void make_plan(const TreeParams &p, int32_t *pre, int32_t *len, uint1
         const int n_cut = __popc(__ballot_sync(kAll, parts > 1));
         if (lane == 0) {
             vars[0] = some;
-            vars[1] = n_cut;
-        }
-    } else if (warp == 0) {
-        const int per = (S + 31) / 32, lo_s = min(S, lane * per), hi_s = min(S, lo_s + per);
-        long long total = 0;
-        int some = 0, longest = 0;
-        for (int s = lo_s; s < hi_s; ++s) {
-            total += len[s];
-            some += len[s] > 0;
-            longest = max(longest, len[s]);
-        }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) {
-            total += __shfl_xor_sync(kAll, total, off);
-            some += __shfl_xor_sync(kAll, some, off);
-            longest = max(longest, __shfl_xor_sync(kAll, longest, off));
-        }
-        int cut_parts;
-        Cuts c = candidate(longest, lane);
-        if ((long long)some * HG < 4 * (int)gridDim.x)
-            for (int s = 0; s < S; ++s) c.take(len[s]);
-        int P = part_size(p, total, some, HG, c, lane);
-        while (true) {   // (more than the cap only where the first case found none)
-            cut_parts = 0;
-            for (int s = lo_s; s < hi_s; ++s)
-                if (len[s] > P) cut_parts += (len[s] + P - 1) / P;
-            if (__reduce_add_sync(kAll, cut_parts) <= p.cap) break;
-            P *= 2;
-        }
-        // counting sort by size class: 0 the cut ones, 1 .. 31 the others, long
-        // ones first; counts[lane][class], a row of 33
-        const int top = min(P, longest);
-        auto cls = [&](int l) { return l > P ? 0 : 1 + (int)((long long)(top - l) * 30 / top); };
-        for (int k = 0; k < 32; ++k) counts[lane * 33 + k] = 0;
-        __syncwarp();
-        for (int s = lo_s; s < hi_s; ++s)
-            if (len[s] > 0) ++counts[lane * 33 + cls(len[s])];
-        __syncwarp();
-        int mine_cls = 0;                // lane = class: where its lanes' sequences start
-        for (int k = 0; k < 32; ++k) mine_cls += counts[k * 33 + lane];
-        const int incl_cls = warp_incl_scan(mine_cls, lane);
-        int at = incl_cls - mine_cls;
-        for (int k = 0; k < 32; ++k) {
-            const int c = counts[k * 33 + lane];
-            counts[k * 33 + lane] = at;
-            at += c;
-        }
-        __syncwarp();
-        const int start = __shfl_sync(kAll, incl_cls, 31), n_cut = __shfl_sync(kAll, incl_cls, 0);
-        for (int s = lo_s; s < hi_s; ++s)
-            if (len[s] > 0) order[counts[lane * 33 + cls(len[s])]++] = (uint16_t)s;
-        __syncwarp();
-        const int n_ord = start, per2 = (n_ord + 31) / 32;
-        const int lo_i = min(n_ord, lane * per2), hi_i = min(n_ord, lo_i + per2);
-        int parts = 0;
-        for (int i = lo_i; i < hi_i; ++i) parts += (len[order[i]] + P - 1) / P;
-        int run = warp_incl_scan(parts, lane) - parts;
-        for (int i = lo_i; i < hi_i; ++i) {
-            pre[i] = run;
-            run += (len[order[i]] + P - 1) / P;
-        }
-        if (hi_i == n_ord) pre[n_ord] = run;   // (lanes past the end hold the total too)
-        if (lane == 0) {
-            vars[0] = n_ord;
             vars[1] = n_cut;
         }
     }
@@ -580,7 +627,7 @@ __device__ __noinline__ void node_tiles(const TreeParams &p, const int32_t *u, c
 
 template <int D, int NQ, bool SCORES>
 __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
-    tree_attention_kernel(const TreeParams p, const __grid_constant__ TreeMaps maps) {
+    tree_attention_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
     using Cfg = TreeCfg<D, NQ>;
     constexpr int NP = Cfg::NP, HALF = Cfg::HALF;
     constexpr int QB = Cfg::QB, SW = Cfg::SW, CQ = Cfg::CQ, ST = SW * 32;
