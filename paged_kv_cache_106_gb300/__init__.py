@@ -636,6 +636,10 @@ def pa_verify_draft(path, path_lens, next_tokens, target_probs, draft_probs, dra
             PA_DTYPE_BF16 if kind is torch.bfloat16 else -1)
     if code < 0:
         raise ValueError(f"target_probs is {kind}: float32, float16 or bfloat16 expected")
+    if draft_probs is not None and draft_probs.shape[1] != vocab:
+        raise ValueError("target_probs and draft_probs differ in width")
+    if path.shape[1] != mq:
+        raise ValueError(f"path is {path.shape[1]} wide, max_q_len {mq}")
     _check(_lib.pa_verify_draft(
         _arg("path", path, i32, n * mq), _arg("path_lens", path_lens, i32, n),
         _arg("next_tokens", next_tokens, i32, n), _arg("target_probs", target_probs, kind, 0),
@@ -665,6 +669,8 @@ def pa_decode_attention_weights(out, weights_out, weights_in, q, k_cache, v_cach
     if weights_in is not None and weights_in.shape[-1] != wl:
         raise ValueError("weights_in and weights_out differ in length")
     c = desc.c
+    if weights_out.shape[-2] != c.num_heads:
+        raise ValueError(f"weights_out has {weights_out.shape[-2]} heads, the cache {c.num_heads}")
     width = c.num_heads * c.head_dim
     cache, sums = c.num_blocks * c.block_size * width, n * c.num_heads * wl
     _check(_lib.pa_decode_attention_weights(
@@ -688,6 +694,8 @@ def pa_evict_select(keep, keep_lens, weights_out, weights_in, ctx_lens, budget: 
     _, heads, wl = weights_in.shape
     if weights_out.shape[1:] != weights_in.shape[1:]:
         raise ValueError("weights_in and weights_out differ in shape")
+    if keep.shape[-1] != budget or keep.shape[-2] != heads:
+        raise ValueError(f"keep is {tuple(keep.shape)}: {heads} heads, {budget} entries expected")
     sums = n * heads * wl
     _check(_lib.pa_evict_select(
         _arg("keep", keep, i32, n * heads * budget), _arg("keep_lens", keep_lens, i32, n),
