@@ -12,34 +12,53 @@
 // by the parts' (m, l, sum).  The weight of position p is 2^(x'_p - m) / l.
 //
 // What bounds it: every key and value is read once for all n rows of a
-// sequence, 4 D bytes against 4 n D operations a position, so up to the 64
-// rows allowed the bytes bound it (64 flops a byte against 286 the tensor
-// cores could do).  The products run on the tensor cores all the same (a
-// row's dot products on the plain pipes would be 16 times slower than the
-// bytes at n = 16): m16n8k16 products with queries in M.
+// sequence, 4 D bytes against 4 n D operations a position, so up to the 64 rows
+// allowed the bytes bound it (64 operations a byte against the 286 that the
+// tensor cores could do in that time).
 //
-// Layout.  One persistent CTA an SM slot: a producer warp streams the unit's
-// blocks by TMA (GH adjacent heads of a block are one box, 128-byte swizzled)
-// into a ring; consumer warp (g, mw) owns head g and query rows
-// [16 mw, 16 mw + 16) for the whole unit, so nothing is combined between
-// warps.  In the swizzled layout every fragment comes by plain 16-byte shared
-// loads without bank conflicts:
-//   * keys (B of S = Q K^T): lane (g, c) takes the 8 dims [16c + 8u, +8) of
-//     token g; a product's k index is any order of the dims that Q shares;
-//   * values (B of O = P V): lane (g, c) takes 8 dims of its four tokens and
-//     interleaves them pairwise (byte permutes), so column g of n-tile e is
-//     dim 8g + e: the accumulators of a lane are 16 consecutive dims.
-// Scores stay in registers from the first product to the second: the
-// accumulator layout of S is the A layout of P.
+// Products (tcgen05, one tile of 128 tokens at a time).  Tokens, of which there
+// are always many, are the 128 lanes of tensor memory and the few rows its
+// columns (N = 16, 32 or 64: the rows padded):
+//     S (tokens x rows)  = K Q^T,     K and Q as they lie, K-major
+//     O (dims x rows)   += V^T P^T,   V and P as they lie, both MN-major
+// so nothing is transposed, 8 rows cost little more than 1, and one thread owns
+// one token's scores (then one dimension of the output).  With queries in the
+// lanes (128 of them, 8 used) the same cases took 242 us instead of 215 (64
+// sequences of 128 to 2048 positions, 4 to 16 nodes, 40 heads of 128) and 282
+// instead of 214 (3 sequences of 40 to 65 thousand, 31 nodes, 32 heads of 64);
+// warp-level products (m16n8k16) 1814 us instead of 762 at 64 nodes (256
+// sequences of 128 to 1536 positions).
 //
-// Rounding: products of fp16 values are exact in the fp32 accumulators; the
-// running maximum is exact, so P is in [0, 1] and enters the second product
-// as fp16 (half a unit in 2^-11 of each weight, like the fp16 output's own
-// rounding); sums and the join of parts are fp32.
+// One persistent CTA an SM.  Its warps:
+//   * producer: names the units (sequence, head, part) and streams their blocks
+//     by TMA, a block of one head a box, 128-byte swizzled, keys and values of a
+//     tile in two stages of a ring that fills what shared memory is left (5 to 12
+//     stages, 160 to 196 KB on their way);
+//   * products: S of tile t + 1, then O of tile t;
+//   * queries: Q of the unit by TMA, and which nodes see each node;
+//   * 4 softmax warps up to 16 rows, 8 above (a token's rows halved: 64 nodes
+//     945 -> 779 us; at 16 rows 8 gave 22.4 instead of 21.9 us for one sequence,
+//     247 instead of 246 us for 64).
+// Scores are taken relative to a reference per row that only moves where a
+// score passes it by 2^8 (then O and the sums are rescaled; P stays below 2^8 in
+// fp16): almost every tile goes without a reduction over its tokens.
 //
-// Work plan (the same in every CTA): sequences longer than P blocks are cut
-// into even parts, P such that the units fill the slots once (few sequences)
-// or about twice over (many); cut sequences first, then the others by size.
+// Rounding: products of fp16 values are exact in the fp32 accumulators; P enters
+// the second product as fp16 (half a unit in 2^-11 of each weight, like the fp16
+// output's own rounding); sums, references and the join of parts are fp32.
+//
+// Work plan (the same in every CTA, no counters to clear): sequences are cut into
+// even parts by part_size; cut ones first, then the others by size, dealt to the
+// CTAs back and forth.  The kernel that joins the parts is launched ahead and
+// waits for this one's end (one sequence: 14.2 instead of 14.5 us).
+//
+// Measured (in a graph; share of the bytes' time at 6.78 TB/s): 64 sequences of
+// 128 to 2048, 4 to 16 nodes, 40 heads of 128: 215 us (98 %); 256 sequences of 128
+// to 1536, 64 nodes: 762 us (91 %; the softmax of 64 rows and the end of each
+// unit, 3.2 of 3.4 thousand clocks a tile, are what bounds it); 3 of 40 to 65
+// thousand, 17 to 31 nodes, 32 heads of 64: 214 us (89 %); 1 of 2048, 8 nodes:
+// 14.1 us against 6.2 (two launches, the plan, one round of loads: latency).
+// Weights form: 64 sequences 220 us (97 %), 2 of 50 to 65 thousand 381 us (93 %).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -991,7 +1010,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                 };
                 scores();
                 // a row's reference moves when a score passes it by more than 2^8
-                bool over = t0 == 0;
+                bool over = false;
                 if (t0 > 0) {
                     float top = -INFINITY;
 #pragma unroll
@@ -1002,7 +1021,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                         }
                     over = top > kRescaleLog2;
                 }
-                if (softmax_any<ST>(over || !ok)) {
+                if (t0 == 0 || softmax_any<ST>(over || !ok)) {
                     if (!softmax_all<ST>(ok)) break;
                     if (t0 > 0) {                        // the scores themselves
 #pragma unroll
@@ -1115,14 +1134,13 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                     ++use_v;
                 }
             }
-            if (!softmax_all<ST>(ok)) break;
-            const bool nodes = node_tile != INT_MAX;
-            if (lane == 0 && !nodes) mbar_arrive(bar_unit_free + 8 * slot);
             // sums over the tokens
             const int first = warp_combine(l, lane, [](float a, float c) { return a + c; });
 #pragma unroll
             for (int i = 0; i < (R + 31) / 32; ++i) red[(warp & 3) * NQ + col0 + first + i] = l[i];
-            softmax_sync<ST>();
+            if (!softmax_all<ST>(ok)) break;
+            const bool nodes = node_tile != INT_MAX;
+            if (lane == 0 && !nodes) mbar_arrive(bar_unit_free + 8 * slot);
             const size_t part_row = ((size_t)part * H + h) * NQ;
             if (tid < (SCORES ? 1 : NQ)) {
                 const float sum = (red[tid] + red[NQ + tid]) + (red[2 * NQ + tid] + red[3 * NQ + tid]);
