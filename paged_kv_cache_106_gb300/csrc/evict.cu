@@ -30,9 +30,15 @@ constexpr unsigned kAll = 0xffffffffu;
 // positions stay in shared memory, longer ones are re-read through L2.  Bound
 // by the barriers between these steps, so short rows take small CTAs, several
 // an SM.
+//
+// Measured: 64 sequences of 256 to 2048 positions x 40 heads, 512 kept: 26 us (11 MB
+// read: 2 us; with the move 214 us, and 237 with 1024 threads a CTA instead of
+// 256, 223 with more histograms instead of ranking).  4 of 20 to 32 thousand, 4096
+// kept: some 45 us, the move 110 (with more histograms 4 us later; a row in
+// shared memory, which leaves one CTA an SM above kCached, 1 us earlier).
 
 constexpr int kBins = 2048;
-constexpr int kFew = 512;            // keys of a bin that are ranked one against another
+constexpr int kFew = 512;            // keys of a bin that are ranked one against another (8 bytes each, where the bins were)
 constexpr int kShort = 4096;         // positions up to which a CTA has 256 threads, else 1024
 constexpr int kCached = 26624;       // positions of a row kept in shared memory (104 KB: two CTAs an SM)
 
@@ -281,10 +287,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Sele
 // once; rows already in place are skipped.  Two forms:
 //   * a list for each head, or a long one: a head of a cache a CTA, 16 threads a
 //     row (D = 128) and so many rows at once, a barrier between loads and stores;
-//   * a short list for all heads (accepted drafts; many layers): a
-//     thread has a column of all heads' rows to itself, needs no barrier, and
-//     moves keys and values of several layers by the same row numbers (finding
-//     them takes longer than moving a row).
+//   * a short list for all heads (accepted drafts; many layers): a thread has a
+//     column of all heads' rows to itself, needs no barrier, and moves keys and
+//     values by the same row numbers (finding them takes longer than moving a
+//     row).  Several layers a CTA, which share that finding, made no difference
+//     (174 us).
+// Measured: 24 layers x 256 sequences of 1 to 8 accepted rows x 40 heads of 128: 174
+// us, 96 % of the bytes' time (by the first form 1641 us: a CTA a head, most of
+// them for a row or two).  64 sequences x 40 heads, 512 rows each of its own list:
+// 187 us, 1.22 GB at 6.5 TB/s.
 
 constexpr int kMoveThreads = 256;
 constexpr int kMaxMoveLayers = 128;
@@ -295,7 +306,6 @@ struct CompactParams {
     const int32_t *src_tables, *dst_tables, *src_lens, *first, *keep, *keep_lens;
     int32_t num_heads, keep_heads, keep_stride, max_blocks, num_blocks, bshift, row_shift;
     int32_t cols, rows, chunk;       // columns and rows a pass of the CTA covers; rows of a chunk
-    int32_t layers, each;            // layers in all, and of a CTA (shared lists)
     int32_t *status;
     uint4 *cache[2 * kMaxMoveLayers];   // keys and values of layer 0, 1, ..
 };
@@ -372,15 +382,13 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kv_kernel(const __grid_c
         uint4 x[kUnroll];
         if (SHARED) {
             if (j0 + a.chunk < len) plan(buf ^ 1, j0 + a.chunk);
-            const int l1 = min(a.layers, (int)(blockIdx.z + 1) * a.each);
-            if (mine)
-                for (int l = blockIdx.z * a.each; l < l1; ++l) {
-                    uint4 y[kUnroll];
-                    load(a.cache[2 * l], buf, x);
-                    load(a.cache[2 * l + 1], buf, y);
-                    store(a.cache[2 * l], buf, x);
-                    store(a.cache[2 * l + 1], buf, y);
-                }
+            if (mine) {
+                uint4 y[kUnroll];
+                load(a.cache[2 * blockIdx.z], buf, x);
+                load(a.cache[2 * blockIdx.z + 1], buf, y);
+                store(a.cache[2 * blockIdx.z], buf, x);
+                store(a.cache[2 * blockIdx.z + 1], buf, y);
+            }
         } else {
             uint4 *cache = a.cache[blockIdx.z];
             if (mine) load(cache, buf, x);
@@ -475,7 +483,6 @@ int launch_compact_kv(void *const *k_caches, void *const *v_caches, int32_t num_
     while ((1 << a.bshift) < d->block_size) ++a.bshift;
     while ((8 << a.row_shift) < d->head_dim) ++a.row_shift;
     a.status = status;
-    a.layers = num_layers;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const unsigned S = (unsigned)n_seqs;
     if (keep_heads > 1 || keep_stride > kShortList) {
@@ -490,10 +497,7 @@ int launch_compact_kv(void *const *k_caches, void *const *v_caches, int32_t num_
         a.chunk = 4;
         const int64_t gx = (columns + a.cols - 1) / a.cols;
         if (gx > INT32_MAX) return fail(PA_ERR_INVALID_ARG, "%s: num_heads * head_dim too large", who);
-        // as many layers a CTA as leave some 30 CTAs an SM
-        a.each = (int)std::max<int64_t>(1, std::min<int64_t>(num_layers, gx * n_seqs * num_layers / 4608));
-        compact_kv_kernel<true><<<dim3((unsigned)gx, S, (unsigned)((num_layers + a.each - 1) / a.each)), kMoveThreads, 0,
-                                  st>>>(a);
+        compact_kv_kernel<true><<<dim3((unsigned)gx, S, (unsigned)num_layers), kMoveThreads, 0, st>>>(a);
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
