@@ -5,9 +5,12 @@
  * The library implements the data-parallel hot path of PagedAttention:
  * a host-side block manager (free-block queue, per-block reference counts,
  * per-sequence block tables with #filled, fork / append / free,
- * copy-on-write of shared last blocks) and three sm_103a CUDA kernels that
+ * copy-on-write of shared last blocks) and the sm_103a CUDA kernels that
  * consume its output -- the fused slot write, the fused block copy and
- * single-query paged decode attention with an optional split-context merge.
+ * single-query paged decode attention with an optional split-context merge,
+ * causal prefill attention, and, for drafted tokens and for a bounded cache,
+ * tree attention, verification, attention that adds up the positions' weights,
+ * selection by weight and the move of kept rows.
  *
  * Sources for the operations (pages are cited by title and section):
  *   [review]   "Efficient Memory Management for Large Language Model Serving
