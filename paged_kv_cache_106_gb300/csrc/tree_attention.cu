@@ -38,7 +38,8 @@
 //   * queries: Q of the unit by TMA, and which nodes see each node;
 //   * 4 softmax warps up to 16 rows, 8 above (a token's rows halved: 64 nodes
 //     945 -> 779 us; at 16 rows 8 gave 22.4 instead of 21.9 us for one sequence,
-//     247 instead of 246 us for 64).
+//     247 instead of 246 us for 64).  Up to 16 rows and with two units a CTA or
+//     more there are two groups of 4 that take units in turn (launch_tree).
 // Scores are taken relative to a reference per row that only moves where a
 // score passes it by 2^8 (then O and the sums are rescaled; P stays below 2^8 in
 // fp16): almost every tile goes without a reduction over its tokens.
@@ -53,12 +54,12 @@
 // waits for this one's end (one sequence: 14.2 instead of 14.5 us).
 //
 // Measured (in a graph; share of the bytes' time at 6.78 TB/s): 64 sequences of
-// 128 to 2048, 4 to 16 nodes, 40 heads of 128: 215 us (98 %); 256 sequences of 128
-// to 1536, 64 nodes: 762 us (91 %; the softmax of 64 rows and the end of each
+// 128 to 2048, 4 to 16 nodes, 40 heads of 128: 217 us (98 %); 256 sequences of 128
+// to 1536, 64 nodes: 767 us (90 %; the softmax of 64 rows and the end of each
 // unit, 3.2 of 3.4 thousand clocks a tile, are what bounds it); 3 of 40 to 65
-// thousand, 17 to 31 nodes, 32 heads of 64: 214 us (89 %); 1 of 2048, 8 nodes:
+// thousand, 17 to 31 nodes, 32 heads of 64: 217 us (88 %); 1 of 2048, 8 nodes:
 // 14.1 us against 6.2 (two launches, the plan, one round of loads: latency).
-// Weights form: 64 sequences 220 us (97 %), 2 of 50 to 65 thousand 381 us (93 %).
+// Weights form: 64 sequences 221 us (97 %), 2 of 50 to 65 thousand 384 us (92 %).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -92,7 +93,7 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHeaderBytes = 256;    // workspace head: number of cut sequences
-constexpr int kUnitSlots = 3;        // units a CTA has open
+constexpr int kUnitSlots = 8;        // units a CTA has open (with 3, 256 sequences of 100 positions took 164 instead of 161 us)
 constexpr int kTile = 128;           // tokens of a tile: the lanes of tensor memory
 constexpr float kRescaleLog2 = 8.f;  // tensor-memory kernel: how far a row's maximum may pass its reference
 
@@ -152,6 +153,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+
+// Whether a barrier's phase is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return r != 0;
 }
 
 // One lane of a warp whose lanes are all here, always the same.
@@ -482,59 +494,65 @@ __device__ __forceinline__ void nodes_seen_by(const TreeParams &p, const SeqRows
 
 constexpr int kMinStages = 4, kMaxStages = 12;
 
-template <int D, int NQ>
+template <int D, int NQ, int G>
 struct TreeCfg {
     static constexpr int NP = D / 64;                        // 64-column panels of a row
     static constexpr int HALF = kTile * D * 2;               // keys or values of a tile: a ring stage
     // softmax warps: a token of the tile a thread, with more than 16 rows two
     // threads a token, each half of the rows; then the warps that stream the
     // ring, issue the products and fetch Q
+    // (SW of them).  Two groups of them take units in turn, so that one's end
+    // (sums, O, output) is behind the other's tiles: see launch_tree.
     static constexpr int SW = NQ == 16 ? 4 : 8, CQ = NQ / (SW / 4);
-    static constexpr int PRODUCER = SW, PRODUCTS = SW + 1, Q_WARP = SW + 2;
-    static constexpr int THREADS = (SW + 3) * 32;
-    // tensor-memory columns: two S, O, O of the tiles that rows see different nodes of
-    static constexpr uint32_t S_COL = 0, O_COL = 2 * NQ, N_COL = 3 * NQ, COLS = 4 * NQ;
+    static constexpr int PRODUCER = SW * G, PRODUCTS = PRODUCER + 1, Q_WARP = PRODUCER + 2;
+    static constexpr int THREADS = (PRODUCER + 3) * 32;
+    // tensor-memory columns: two S, then for each group O, O of the tiles that
+    // rows see different nodes of (a power of two in all)
+    static constexpr uint32_t S_COL = 0, O_COL = 2 * NQ, COLS = G == 2 ? 8 * NQ : 4 * NQ;
     static constexpr int BARS = 0;                           // full, empty; units; q, s, p, seen, o, done
-    static constexpr int VARS = BARS + (2 * kMaxStages + 3 * kUnitSlots + 2 * 2 + 2 + 2 + 1 + 1) * 8;
+    static constexpr int VARS = BARS + (2 * kMaxStages + 3 * kUnitSlots + 2 * 2 + 4 + 2 + 2 + 1) * 8;
     static constexpr int UNITS = (VARS + 16 + 15) / 16 * 16;
-    static constexpr int SEEN = UNITS + kUnitSlots * 64;     // 64 x u64 per slot
-    static constexpr int RED = SEEN + kUnitSlots * 64 * 8;   // per 32 tokens and row
-    static constexpr int REF = RED + 4 * NQ * 4;             // reference maxima, corrections
-    static constexpr int PLAN = REF + 2 * NQ * 4;            // pre[S+1], len[S], order[S]
+    static constexpr int SEEN = UNITS + kUnitSlots * 64;     // NQ x u64 per slot
+    static constexpr int RED = SEEN + kUnitSlots * NQ * 8;   // per 32 tokens and row
+    static constexpr int REF = RED + G * 4 * NQ * 4;    // reference maxima, corrections
+    static constexpr int PLAN = REF + G * 2 * NQ * 4;   // pre[S+1], len[S], order[S]
     static constexpr int Q_BYTES = NQ * D * 2;               // [panel][row][128 bytes]
     static constexpr int QB = Q_BYTES > 8192 ? 1 : 2;        // buffers of it
     static constexpr int P_BYTES = kTile * 128;              // [token][128 bytes], rows of 64 columns
-    static int plan_bytes(int S) { return (S + 1) * 4 + S * 4 + (S + 1) / 2 * 4; }
-    static int bytes(int S, int stages) {
-        return PLAN + plan_bytes(S) + 1024 + QB * Q_BYTES + 2 * P_BYTES + stages * HALF;
+    // node_tiles' numbers: a group's own, or where P is
+    static constexpr int ODD_BYTES = G == 2 ? NQ * kTile * 4 : 0;
+    __host__ __device__ static constexpr int plan_bytes(int S) { return (S + 1) * 4 + S * 4 + (S + 1) / 2 * 4; }
+    static constexpr int bytes(int S, int stages) {
+        return (PLAN + plan_bytes(S) + 1023) / 1024 * 1024 + G * ODD_BYTES + QB * Q_BYTES + 2 * P_BYTES +
+               stages * HALF;
     }
 };
 
-// One barrier of the softmax warps (N threads).  (A warp comes to a barrier,
-// and to the loads and stores of tensor memory, with all its lanes together:
-// the instructions are undefined otherwise, and lanes that parted at a branch
-// before need not have met again by themselves.)
+// One barrier of a group of softmax warps (N threads).  (A warp comes to a
+// barrier, and to the loads and stores of tensor memory, with all its lanes
+// together: the instructions are undefined otherwise, and lanes that parted at a
+// branch before need not have met again by themselves.)
 template <int N>
-__device__ __forceinline__ void softmax_sync() {
+__device__ __forceinline__ void softmax_sync(int group) {
     __syncwarp();
-    asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(N) : "memory");
 }
 // The same; whether v held in any (all) of their threads.
 template <int N>
-__device__ __forceinline__ bool softmax_any(bool v) {
+__device__ __forceinline__ bool softmax_any(int group, bool v) {
     uint32_t r;
     __syncwarp();
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\t"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v), "n"(N)
+        : "r"((uint32_t)v), "r"(1 + group), "n"(N)
         : "memory");
     return r != 0;
 }
 template <int N>
-__device__ __forceinline__ bool softmax_all(bool v) {
-    return !softmax_any<N>(!v);
+__device__ __forceinline__ bool softmax_all(int group, bool v) {
+    return !softmax_any<N>(group, !v);
 }
 
 // Combines N values over a warp's lanes: on return v[0 .. max(N / 32, 1)) are
@@ -569,13 +587,14 @@ __device__ __forceinline__ int warp_combine(float (&v)[N], int lane, Op op) {
 // accumulator of their own, so that the rest of a long unit needs no second
 // pass.  A look at every tile's values instead costs each unit without such
 // values: 256 sequences of 64 nodes took 820 us with it, 788 us so.
-template <int D, int NQ>
+template <int D, int NQ, int G>
 __device__ __noinline__ void node_tiles(const TreeParams &p, const int32_t *u, const uint64_t *seen,
                                         const float *ref, float *buf, bool odd, float *o) {
-    using Cfg = TreeCfg<D, NQ>;
+    using Cfg = TreeCfg<D, NQ, G>;
     constexpr int CQ = Cfg::CQ, ST = Cfg::SW * 32;
     const int s = u[0], h = u[1], tok_first = u[4], n_tok = u[5], base = u[6], n = u[7], row0 = u[8];
-    const int H = p.num_heads, tok = threadIdx.x & 127, lane = threadIdx.x & 31, col0 = (threadIdx.x >> 7) * CQ;
+    const int group = G == 2 ? threadIdx.x >> 7 : 0, id = threadIdx.x - group * ST;
+    const int H = p.num_heads, tok = id & 127, lane = id & 31, col0 = (id >> 7) * CQ;
     const int32_t *table = p.block_tables + (size_t)s * p.max_blocks;
     // where a position's row is in the caches, -1: in no block of the pool
     auto at = [&](int pos) {
@@ -617,7 +636,7 @@ __device__ __noinline__ void node_tiles(const TreeParams &p, const int32_t *u, c
                 *to = x;
             }
         }
-        softmax_sync<ST>();
+        softmax_sync<ST>(group);
         if (__any_sync(kAll, odd))
             for (int j0 = 0; j0 < here; j0 += 32) {
                 // a token a lane: where it is, and who sees it
@@ -633,40 +652,37 @@ __device__ __noinline__ void node_tiles(const TreeParams &p, const int32_t *u, c
                         if ((by >> i) & 1) sum[i] = fmaf(buf[(col0 + i) * kTile + j0 + j], v, sum[i]);
                 }
             }
-        softmax_sync<ST>();
+        softmax_sync<ST>(group);
     }
     if (odd) {
 #pragma unroll
         for (int i = 0; i < CQ; ++i) o[i] = sum[i];
     }
-    for (int i = threadIdx.x; i < NQ * kTile; i += ST) buf[i] = 0.f;   // (as P: finite)
+    for (int i = id; i < NQ * kTile; i += ST) buf[i] = 0.f;   // (as P: finite)
     fence_proxy_async_smem();
-    softmax_sync<ST>();
+    softmax_sync<ST>(group);
 }
 
-template <int D, int NQ, bool SCORES>
-__global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
+template <int D, int NQ, bool SCORES, int G>
+__global__ void __launch_bounds__((TreeCfg<D, NQ, G>::THREADS), 1)
     tree_attention_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
-    using Cfg = TreeCfg<D, NQ>;
+    using Cfg = TreeCfg<D, NQ, G>;
     constexpr int NP = Cfg::NP, HALF = Cfg::HALF;
     constexpr int QB = Cfg::QB, SW = Cfg::SW, CQ = Cfg::CQ, ST = SW * 32;
     constexpr int R = SCORES ? 1 : CQ;                   // rows a softmax thread works on
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t bar_full = smem_addr(smem + Cfg::BARS), bar_empty = bar_full + kMaxStages * 8;
     const uint32_t bar_unit = bar_empty + kMaxStages * 8, bar_unit_free = bar_unit + kUnitSlots * 8;
     const uint32_t bar_q = bar_unit_free + kUnitSlots * 8, bar_q_free = bar_q + 16, bar_s = bar_q_free + 16,
-                   bar_p = bar_s + 16, bar_seen = bar_p + 16, bar_o = bar_seen + 8 * kUnitSlots, bar_done = bar_o + 8;
+                   bar_p = bar_s + 32, bar_seen = bar_p + 16, bar_o = bar_seen + 8 * kUnitSlots, bar_done = bar_o + 16;
     int32_t *vars = reinterpret_cast<int32_t *>(smem + Cfg::VARS);    // [2]: tensor-memory address
     int32_t *units = reinterpret_cast<int32_t *>(smem + Cfg::UNITS);
     uint64_t *seen = reinterpret_cast<uint64_t *>(smem + Cfg::SEEN);
-    float *red = reinterpret_cast<float *>(smem + Cfg::RED);
-    float *ref = reinterpret_cast<float *>(smem + Cfg::REF), *corr = ref + NQ;
     const int S = p.n_seqs, H = p.num_heads;
     int32_t *pre = reinterpret_cast<int32_t *>(smem + Cfg::PLAN);
     int32_t *len = pre + S + 1;
     uint16_t *order = reinterpret_cast<uint16_t *>(len + S);
-    uint8_t *tiles_at = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(order + S) + 1023) & ~uintptr_t(1023));
+    uint8_t *tiles_at = smem + (Cfg::PLAN + Cfg::plan_bytes(S) + 1023) / 1024 * 1024;
     // (the shuffles here and in the products' warp tell the compiler that a warp's lanes agree)
     const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
     const int stages = p.stages, bshift = p.bshift, B = 1 << bshift, bps = kTile >> bshift;
@@ -687,12 +703,12 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
             mbar_init(bar_q + 8 * i, 1);
             mbar_init(bar_q_free + 8 * i, 1);
         }
-        mbar_init(bar_s, 1);
-        mbar_init(bar_s + 8, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(bar_s + 8 * i, 1);   // group, buffer
         mbar_init(bar_p, SW);
         mbar_init(bar_p + 8, SW);
         for (int i = 0; i < kUnitSlots; ++i) mbar_init(bar_seen + 8 * i, 1);
         mbar_init(bar_o, 1);
+        mbar_init(bar_o + 8, 1);
         mbar_init(bar_done, 1);
         fence_barrier_init();
     }
@@ -720,7 +736,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
         const uint64_t policy = l2_evict_first_policy();
         const uint32_t blk_bytes = (uint32_t)D * 2u << bshift;
         const int run = B >> 3;                          // 8-row groups of a block's head
-        int st = 0, k_unit = 0, issued = 0;
+        int st = 0, k_unit = 0, issued = 0, tile = 0;    // (tile: of all units so far)
         uint32_t use = 0;
         struct Pending {
             int ticket, s, h, gp, parts, b0, nb, tbl;
@@ -761,10 +777,11 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
             return ok;
         };
         // Units in order of size, back and forth over the CTAs.
-        const int G = gridDim.x;
+        const int n_ctas = gridDim.x;
         Pending cur = prepare(blockIdx.x);
+        int ends = 0;
         while (true) {
-            const bool last = cur.ticket >= n_units;     // one more descriptor: the end
+            const bool last = cur.ticket >= n_units;     // one more descriptor (a group): the end
             const int slot = k_unit % kUnitSlots, slot_use = k_unit / kUnitSlots;
             if (slot_use > 0)
                 ok = mbar_wait_bounded(bar_unit_free + 8 * slot, (uint32_t)(slot_use - 1) & 1u, p.status, true);
@@ -773,22 +790,25 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
             int32_t *u = units + slot * 16;
             const int base = cur.r.ctx - cur.r.n;
             cur.nb = min(cur.nb, ((cur.r.ctx + B - 1) >> bshift) - cur.b0);
+            const int n_tok = last ? 0 : min(cur.r.ctx, (cur.b0 + cur.nb) << bshift) - (cur.b0 << bshift);
             if (lane == 0) {
-                const int end = min(cur.r.ctx, (cur.b0 + cur.nb) << bshift);
                 u[0] = cur.s;
                 u[1] = cur.h;
                 u[2] = cur.gp;
                 u[3] = cur.parts;
                 u[4] = cur.b0 << bshift;                     // first token
-                u[5] = last ? 0 : end - u[4];                // tokens
+                u[5] = n_tok;                                // tokens
                 u[6] = base;
                 u[7] = cur.r.n;
                 u[8] = cur.r.row0;
+                u[9] = tile;
             }
             if (lane == 0) mbar_arrive(bar_unit + 8 * slot);
             ++k_unit;
-            if (last) break;
-            const Pending nxt = prepare(k_unit * G + (k_unit & 1 ? G - 1 - (int)blockIdx.x : (int)blockIdx.x));
+            if (last && (++ends == G)) break;
+            if (last) continue;
+            tile += (n_tok + kTile - 1) / kTile;
+            const Pending nxt = prepare(k_unit * n_ctas + (k_unit & 1 ? n_ctas - 1 - (int)blockIdx.x : (int)blockIdx.x));
             const int32_t *trow = p.block_tables + (size_t)cur.s * p.max_blocks + cur.b0;
             int tbl = cur.tbl;
             for (int b = 0; b < cur.nb; b += bps) {
@@ -851,7 +871,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                     tma_load_3d(sQ + buf * Cfg::Q_BYTES + pn * NQ * 128, &maps.q, pn * 64, h, r.row0,
                                 bar_q + 8 * buf);
             }
-            if (edge) nodes_seen_by<SCORES>(p, r, lane, seen + slot * 64);
+            if (edge) nodes_seen_by<SCORES>(p, r, lane, seen + slot * NQ);
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar_seen + 8 * slot);
@@ -874,7 +894,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
         constexpr uint32_t idO = tc::idesc_f16(128, NQ, true) | (1u << 15);   // both MN-major
         int st = 0, st_v = 1;            // stage of the next keys; of the next values
         uint32_t use = 0, use_v = 0, gs = 0, gp = 0;   // tiles whose S, whose O was issued
-        uint32_t q_buf = 0;
+        uint32_t q_buf = 0, s_set = 0;   // of the unit whose S is issued: its Q, its group
         auto wait = [&](uint32_t bar, uint32_t parity) {
             ok = __all_sync(kAll, ok && mbar_wait_bounded(bar, parity, p.status, true));
             return ok;
@@ -899,44 +919,88 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                     tc::mma_ss(d, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
                                dq + (((kk >> 2) * NQ * 128 + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
                 tc::commit(bar_empty + 8 * st);
-                tc::commit(bar_s + 8 * (gs & 1));
+                tc::commit(bar_s + 16 * s_set + 8 * (gs & 1));
                 if (last) tc::commit(bar_q_free + 8 * q_buf);
             }
             __syncwarp();
             ++gs;
             step(st, use);
         };
-        for (uint32_t k = 0;; ++k) {
-            const int slot = k % kUnitSlots;
-            if (!wait(bar_unit + 8 * slot, (k / kUnitSlots) & 1u)) break;
-            const int n_tiles = __shfl_sync(kAll, (units[slot * 16 + 5] + kTile - 1) / kTile, 0);
-            const int node_tile = __shfl_sync(kAll, first_node_tile(slot), 0);
-            if (lane == 0) mbar_arrive(bar_unit_free + 8 * slot);
-            if (n_tiles == 0) break;
-            q_buf = k % QB;
-            if (!wait(bar_q + 8 * q_buf, (k / QB) & 1u)) break;
-            issue_s(n_tiles == 1);
-            for (int t = 0; ok && t < n_tiles; ++t) {
-                if (t + 1 < n_tiles) issue_s(t + 2 == n_tiles);
-                if (!wait(bar_full + 8 * st_v, use_v & 1u) || !wait(bar_p + 8 * (gp & 1), (gp >> 1) & 1u)) break;
-                tc::fence_after();
-                // O (dims x rows) += V^T P^T
-                const uint64_t dv = tc::smem_desc(ring + st_v * HALF, 1024, 1024u * NP);
-                const uint64_t dp = tc::smem_desc(sP + (gp & 1) * Cfg::P_BYTES, 1024, 1024);
-                const uint32_t d = tmem + (t < node_tile ? Cfg::O_COL : Cfg::N_COL);
-                const uint32_t more = t > 0 && t != node_tile ? 1u : 0u;
-                if (elect_one()) {
+        // O (dims x rows) += V^T P^T: tile t of n of the unit of a group
+        auto issue_o = [&](int t, int n, int node_tile, uint32_t group) {
+            if (!wait(bar_full + 8 * st_v, use_v & 1u) || !wait(bar_p + 8 * (gp & 1), (gp >> 1) & 1u)) return;
+            tc::fence_after();
+            const uint64_t dv = tc::smem_desc(ring + st_v * HALF, 1024, 1024u * NP);
+            const uint64_t dp = tc::smem_desc(sP + (gp & 1) * Cfg::P_BYTES, 1024, 1024);
+            const uint32_t d = tmem + Cfg::O_COL + (2 * group + (t < node_tile ? 0 : 1)) * NQ;
+            const uint32_t more = t > 0 && t != node_tile ? 1u : 0u;
+            if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_ss(d, dv + ((kk * 2048u * NP) >> 4), dp + ((kk * 2048u) >> 4), idO, kk > 0 ? 1u : more);
-                    tc::commit(bar_empty + 8 * st_v);
-                    if (t + 1 == n_tiles) tc::commit(bar_o);
-                }
-                __syncwarp();
-                ++gp;
-                step(st_v, use_v);
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    tc::mma_ss(d, dv + ((kk * 2048u * NP) >> 4), dp + ((kk * 2048u) >> 4), idO, kk > 0 ? 1u : more);
+                tc::commit(bar_empty + 8 * st_v);
+                if (t + 1 == n) tc::commit(bar_o + 8 * group);
             }
-            if (!ok) break;
+            __syncwarp();
+            ++gp;
+            step(st_v, use_v);
+        };
+        uint32_t k = 0;                                  // units begun
+        int ns = 0, node_s = 0;                          // the last one's tiles, its first with nodes
+        // Begins the next unit; false: there is none.
+        auto open = [&]() {
+            const int slot = k % kUnitSlots;
+            ns = 0;
+            if (!wait(bar_unit + 8 * slot, (k / kUnitSlots) & 1u)) return false;
+            ns = __shfl_sync(kAll, (units[slot * 16 + 5] + kTile - 1) / kTile, 0);
+            node_s = __shfl_sync(kAll, first_node_tile(slot), 0);
+            if (lane == 0) mbar_arrive(bar_unit_free + 8 * slot);
+            q_buf = k % QB;
+            s_set = k % G;
+            return ns > 0 && wait(bar_q + 8 * q_buf, (k++ / QB) & 1u);
+        };
+        if constexpr (G == 1) {
+            while (open()) {
+                issue_s(ns == 1);
+                for (int t = 0; ok && t < ns; ++t) {
+                    if (t + 1 < ns) issue_s(t + 2 == ns);
+                    issue_o(t, ns, node_s, 0);
+                }
+            }
+        } else {
+            // S goes ahead into the next unit, the other group's, where that is
+            // at hand.  (One place for each product: with a copy for every case
+            // their instructions were waited for, 158 us instead of 151 for 256
+            // sequences of 100 positions.)
+            int ts = 0, to = 0, no = 0, node_o = 0;      // next tile of S's unit; of O's, its tiles
+            int n_before = 0, node_before = 0;           // of the unit before S's
+            uint32_t k_o = 0;                            // units whose O was begun
+            auto at_hand = [&]() {
+                return __all_sync(kAll, mbar_test(bar_unit + 8 * (k % kUnitSlots), (k / kUnitSlots) & 1u) &&
+                                            mbar_test(bar_q + 8 * (k % QB), (k / QB) & 1u) &&
+                                            mbar_test(bar_full + 8 * st, use & 1u));
+            };
+            while (ok) {
+                if (ts == ns && (gs == gp || at_hand())) {
+                    n_before = ns;
+                    node_before = node_s;
+                    ts = 0;
+                    if (!open()) break;                  // (the end has no Q: never at hand before O is done)
+                }
+                if (ts < ns && gs - gp < 2) {
+                    issue_s(++ts == ns);
+                    if (gs - gp < 2) continue;
+                }
+                if (to == no) {
+                    const bool latest = k_o + 1 == k;
+                    to = 0;
+                    no = latest ? ns : n_before;
+                    node_o = latest ? node_s : node_before;
+                    ++k_o;
+                }
+                issue_o(to, no, node_o, (k_o - 1) % G);
+                ++to;
+            }
         }
         if (elect_one()) {
             if (!ok) report(p.status, PA_ERR_TIMEOUT);
@@ -948,12 +1012,18 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
         // Thread = token of the tile (then, for O, dimension of the head) and
         // CQ of the rows.  The warps go through barriers together: a wait that
         // fails only clears ok until the next vote.
-        const int tok = tid & 127, col0 = (warp >> 2) * CQ;
+        const int group = G == 2 ? warp >> 2 : 0, id = tid - group * ST;
+        const int tok = id & 127, col0 = (id >> 7) * CQ;
+        float *red = reinterpret_cast<float *>(smem + Cfg::RED) + group * 4 * NQ;
+        float *ref = reinterpret_cast<float *>(smem + Cfg::REF) + group * 2 * NQ, *corr = ref + NQ;
+        const uint32_t o_col = Cfg::O_COL + group * 2 * NQ;
+        // (this group's, so that a wait for a tile to come cannot take an earlier
+        // tile of the other group's for it)
+        uint32_t s_phase = 0;                            // parities of this group's S barriers
+        float *odd_at = reinterpret_cast<float *>(                // for node_tiles
+            tiles_at + stages * HALF + (G == 2 ? 2 * Cfg::P_BYTES + QB * Cfg::Q_BYTES + group * Cfg::ODD_BYTES : 0));
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float qs = p.qscale;
-        uint32_t g = 0;                                  // tiles so far
-        int st_v = 1;                                    // stage of the tile's values
-        uint32_t use_v = 0;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             ok = __all_sync(kAll, ok && mbar_wait_bounded(bar, parity, p.status, true));
         };
@@ -967,15 +1037,16 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
 #pragma unroll
             for (int i = 0; i < CQ; ++i) v[i] = __uint_as_float(r[i]);
         };
-        for (uint32_t k = 0;; ++k) {
+        for (uint32_t k = group;; k += G) {
             const int slot = k % kUnitSlots;
             wait(bar_unit + 8 * slot, (k / kUnitSlots) & 1u);
-            if (!softmax_all<ST>(ok)) break;
+            if (!softmax_all<ST>(group, ok)) break;
             const int32_t *u = units + slot * 16;
             const int s = u[0], h = u[1], part = u[2], parts = u[3], tok_first = u[4], n_tok = u[5], base = u[6],
                       n = u[7], row0 = u[8];
             if (n_tok <= 0) break;                       // the end
             const int have = n - col0;                   // rows of this thread's that exist
+            uint32_t g = u[9];                           // tile, counted over all units
             const int node_tile = first_node_tile(slot);
             bool knows = false;                          // who sees the nodes is there
             float l[R], off[R];                          // running sums; minus the rows' references
@@ -985,7 +1056,8 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                 const int nv = min(kTile, n_tok - t0);
                 const int pos = tok_first + t0 + tok;
                 const uint32_t b = g & 1;
-                wait(bar_s + 8 * b, (g >> 1) & 1u);
+                wait(bar_s + 16 * group + 8 * b, (G == 1 ? g >> 1 : s_phase >> b) & 1u);
+                if (G == 2) s_phase ^= 1u << b;
                 tc::fence_after();
                 if (tok_first + t0 + kTile > base && !knows) {
                     wait(bar_seen + 8 * slot, (k / kUnitSlots) & 1u);
@@ -1002,7 +1074,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                     if (tok_first + t0 + kTile > base || nv < kTile) {
                         // who sees this position: every row before the nodes, then
                         // the node itself and its descendants; none past the end
-                        const uint64_t v = (tok >= nv ? 0ull : pos < base ? ~0ull : seen[slot * 64 + pos - base]) >> col0;
+                        const uint64_t v = (tok >= nv ? 0ull : pos < base ? ~0ull : seen[slot * NQ + pos - base]) >> col0;
 #pragma unroll
                         for (int i = 0; i < R; ++i)
                             if (!((v >> i) & 1)) y[i] = -INFINITY;
@@ -1021,8 +1093,8 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                         }
                     over = top > kRescaleLog2;
                 }
-                if (t0 == 0 || softmax_any<ST>(over || !ok)) {
-                    if (!softmax_all<ST>(ok)) break;
+                if (t0 == 0 || softmax_any<ST>(group, over || !ok)) {
+                    if (!softmax_all<ST>(group, ok)) break;
                     if (t0 > 0) {                        // the scores themselves
 #pragma unroll
                         for (int i = 0; i < R; ++i) off[i] = 0.f;
@@ -1034,16 +1106,16 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                     const int first = warp_combine(m, lane, [](float a, float c) { return fmaxf(a, c); });
 #pragma unroll
                     for (int i = 0; i < (R + 31) / 32; ++i) red[(warp & 3) * NQ + col0 + first + i] = m[i];
-                    softmax_sync<ST>();
-                    if (tid < (SCORES ? 1 : NQ)) {
-                        const float top = fmaxf(fmaxf(red[tid], red[NQ + tid]), fmaxf(red[2 * NQ + tid], red[3 * NQ + tid]));
+                    softmax_sync<ST>(group);
+                    if (id < (SCORES ? 1 : NQ)) {
+                        const float top = fmaxf(fmaxf(red[id], red[NQ + id]), fmaxf(red[2 * NQ + id], red[3 * NQ + id]));
                         // (a row that has seen nothing yet has reference -2^100: its
                         // terms, if any come, are rescaled from 0)
-                        const float old = t0 ? ref[tid] : -0x1p100f, now = top > old + kRescaleLog2 ? top : old;
-                        ref[tid] = now;
-                        corr[tid] = ex2(old - now);
+                        const float old = t0 ? ref[id] : -0x1p100f, now = top > old + kRescaleLog2 ? top : old;
+                        ref[id] = now;
+                        corr[id] = ex2(old - now);
                     }
-                    softmax_sync<ST>();
+                    softmax_sync<ST>(group);
 #pragma unroll
                     for (int i = 0; i < R; ++i) off[i] = -ref[col0 + i];
                     if (t0 > 0) {
@@ -1051,21 +1123,21 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                         for (int i = 0; i < R; ++i) l[i] *= corr[col0 + i];
                         // O, complete up to the tile before once that gave its
                         // values' stage back
-                        const int st_o = st_v >= 2 ? st_v - 2 : st_v - 2 + stages;
-                        wait(bar_empty + 8 * st_o, (st_v >= 2 ? use_v : use_v - 1) & 1u);
+                        const uint32_t v = 2 * g - 1;            // (stage 2 t + 1 of all holds tile t's)
+                        wait(bar_empty + 8 * (v % stages), (v / stages) & 1u);
                         tc::fence_after();
 #pragma unroll 1
                         for (int half = node_tile == 0; half <= (t0 > node_tile * (int64_t)kTile); ++half) {
                             float o[CQ];
-                            load_cols(Cfg::O_COL + half * NQ, o);
+                            load_cols(o_col + half * NQ, o);
 #pragma unroll
                             for (int i = 0; i < R; ++i) o[i] *= corr[col0 + i];
                             uint32_t r[CQ];
 #pragma unroll
                             for (int i = 0; i < CQ; ++i) r[i] = __float_as_uint(o[i]);
                             __syncwarp();
-                            if constexpr (CQ == 16) tc::st16(lane_base + Cfg::O_COL + half * NQ + col0, r);
-                            else tc::st32(lane_base + Cfg::O_COL + half * NQ + col0, r);
+                            if constexpr (CQ == 16) tc::st16(lane_base + o_col + half * NQ + col0, r);
+                            else tc::st32(lane_base + o_col + half * NQ + col0, r);
                         }
                         tc::wait_st();
                     }
@@ -1111,7 +1183,8 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                                      : "memory");
                 if (nv < kTile) {
                     // values past the end meet P = 0 and have to be finite: zeros
-                    wait(bar_full + 8 * st_v, use_v & 1u);
+                    const uint32_t v = 2 * g + 1, st_v = v % stages;
+                    wait(bar_full + 8 * st_v, (v / stages) & 1u);
                     if (tok >= nv && col0 == 0) {
                         const uint32_t row = ring + st_v * HALF + (uint32_t)(tok >> 3) * (NP * 1024u) +
                                              (uint32_t)(tok & 7) * 128u;
@@ -1128,52 +1201,47 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ>::THREADS), 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_p + 8 * b);
                 ++g;
-                st_v += 2;
-                if (st_v >= stages) {
-                    st_v -= stages;
-                    ++use_v;
-                }
             }
             // sums over the tokens
             const int first = warp_combine(l, lane, [](float a, float c) { return a + c; });
 #pragma unroll
             for (int i = 0; i < (R + 31) / 32; ++i) red[(warp & 3) * NQ + col0 + first + i] = l[i];
-            if (!softmax_all<ST>(ok)) break;
+            if (!softmax_all<ST>(group, ok)) break;
             const bool nodes = node_tile != INT_MAX;
             if (lane == 0 && !nodes) mbar_arrive(bar_unit_free + 8 * slot);
             const size_t part_row = ((size_t)part * H + h) * NQ;
-            if (tid < (SCORES ? 1 : NQ)) {
-                const float sum = (red[tid] + red[NQ + tid]) + (red[2 * NQ + tid] + red[3 * NQ + tid]);
-                corr[tid] = 1.f / sum;
-                if (parts > 1 && tid < n) p.ws_ml[part_row + tid] = make_float2(ref[tid], sum);
+            if (id < (SCORES ? 1 : NQ)) {
+                const float sum = (red[id] + red[NQ + id]) + (red[2 * NQ + id] + red[3 * NQ + id]);
+                corr[id] = 1.f / sum;
+                if (parts > 1 && id < n) p.ws_ml[part_row + id] = make_float2(ref[id], sum);
                 if (SCORES && parts == 1) p.ml_one[(size_t)s * H + h] = make_float2(ref[0], sum);
             }
-            softmax_sync<ST>();
-            wait(bar_o, k & 1u);
+            softmax_sync<ST>(group);
+            wait(bar_o + 8 * group, (k / G) & 1u);
             tc::fence_after();
             float o[CQ];
             if (!nodes) {
-                load_cols(Cfg::O_COL, o);
+                load_cols(o_col, o);
             } else {
-                load_cols(Cfg::N_COL, o);
+                load_cols(o_col + NQ, o);
                 // (0 times a value that is not finite leaves no row's sum finite)
                 bool odd = tok < D && have > 0 && !isfinite(o[0]);
-                const bool some = softmax_any<ST>(odd);
+                const bool some = softmax_any<ST>(group, odd);
                 if (some) {
 #pragma unroll
                     for (int i = 0; i < CQ; ++i) odd = odd && (i >= have || !isfinite(o[i]));
                     float again[CQ];
 #pragma unroll
                     for (int i = 0; i < CQ; ++i) again[i] = o[i];
-                    node_tiles<D, NQ>(p, u, seen + slot * 64, ref,
-                                      reinterpret_cast<float *>(tiles_at + stages * HALF), odd, again);
+                    node_tiles<D, NQ, G>(p, u, seen + slot * NQ, ref,
+                                      odd_at, odd, again);
 #pragma unroll
                     for (int i = 0; i < CQ; ++i) o[i] = again[i];
                 }
                 if (lane == 0) mbar_arrive(bar_unit_free + 8 * slot);
                 if (node_tile > 0) {
                     float before[CQ];
-                    load_cols(Cfg::O_COL, before);
+                    load_cols(o_col, before);
 #pragma unroll
                     for (int i = 0; i < CQ; ++i) o[i] += before[i];
                 }
@@ -1449,10 +1517,10 @@ cudaError_t launch_after(void (*kern)(Args...), dim3 grid, cudaStream_t st, Args
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, int NQ, bool SCORES>
-int launch_tree(TreeParams p, const TreeMaps &maps, const char *who, cudaStream_t st) {
-    using Cfg = TreeCfg<D, NQ>;
-    auto kern = tree_attention_kernel<D, NQ, SCORES>;
+template <int D, int NQ, bool SCORES, int G>
+int launch_groups(TreeParams p, const TreeMaps &maps, const char *who, cudaStream_t st) {
+    using Cfg = TreeCfg<D, NQ, G>;
+    auto kern = tree_attention_kernel<D, NQ, SCORES, G>;
     constexpr int kBytes = 227 * 1024;
     static std::once_flag once[kMaxDevs];
     static cudaError_t err[kMaxDevs];
@@ -1465,13 +1533,25 @@ int launch_tree(TreeParams p, const TreeMaps &maps, const char *who, cudaStream_
     if (err[dev] != cudaSuccess)
         return fail(PA_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(err[dev]));
     p.stages = std::min(kMaxStages, (kBytes - Cfg::bytes(p.n_seqs, 0)) / Cfg::HALF);
-    static_assert((227 * 1024 - TreeCfg<128, 64>::PLAN - 10 * PA_TREE_MAX_SEQS - 8 - 1024 - TreeCfg<128, 64>::Q_BYTES -
-                   2 * TreeCfg<128, 64>::P_BYTES) / TreeCfg<128, 64>::HALF >= kMinStages,
+    static_assert((kBytes - Cfg::bytes(PA_TREE_MAX_SEQS, 0)) / Cfg::HALF >= kMinStages,
                   "room beside the largest batch's plan");
     kern<<<sm_count(), Cfg::THREADS, Cfg::bytes(p.n_seqs, p.stages), st>>>(p, maps);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     return PA_OK;
+}
+
+// Two groups of softmax warps where sequences make two units or more a CTA without
+// being cut: 256 sequences x 40 heads of 100 positions 151 us instead of 204, 4096 x
+// 2 of 40 137 instead of 170, and no difference where units are long (64 sequences,
+// 1000 on average: 218 both).  One where each CTA has a unit or two, all long: 8
+// heads' 20000 positions 21.2 us instead of 23.3.  Above 16 rows two groups'
+// registers do not fit.
+template <int D, int NQ, bool SCORES>
+int launch_tree(const TreeParams &p, const TreeMaps &maps, const char *who, cudaStream_t st) {
+    if constexpr (NQ == 16)
+        if ((int64_t)p.n_seqs * p.num_heads >= 2 * sm_count()) return launch_groups<D, NQ, SCORES, 2>(p, maps, who, st);
+    return launch_groups<D, NQ, SCORES, 1>(p, maps, who, st);
 }
 
 // Checks and the main launch that both entry points share.
