@@ -30,31 +30,24 @@ def _sees(parents, t):
 # ------------------------------------------------- values that are not finite
 
 
-@pytest.mark.parametrize("D,B", [(64, 8), (64, 32), (128, 16)])
-@pytest.mark.parametrize("n", [2, 13, 32, 64])
-@pytest.mark.parametrize("chain", [False, True])
-def test_tree_attention_unseen_values_that_are_not_finite(D, B, n, chain):
-    """Infinities and NaN in the keys or values of some nodes: rows that see them
-    have them in their output, the others stay within the tolerance of the
-    evaluation without, and equal it in the dimensions without such values.
-    Contexts put the nodes in one tile of 128 positions, across two, and behind
-    a context in many parts."""
-    H, ctx = 3, [n, 100 + n, 128 + n // 2, 256, 9000 + n]
-    b = Batch(D + n, ctx, [n] * len(ctx), H, D, B, scale_q=2.0)
-    up = None if chain else b.forest(n)
+def _plant_and_check(b, up, seed, sequences):
+    """Puts infinities and NaN into the keys or values of some nodes of some
+    sequences: rows that see them have them in their output, the others stay
+    within the tolerance of the evaluation without, and equal it in the
+    dimensions without such values."""
     clean = b.run(up).float()
-    r = np.random.default_rng(n)
+    r = np.random.default_rng(seed)
     odd = [math.inf, -math.inf, math.nan]
     want, k, v = clean.clone(), b.k.clone(), b.v.clone()
     hit = torch.zeros_like(want, dtype=torch.bool)
-    for i, c in enumerate(ctx):
-        a = int(b.starts[i])
+    for i in sequences:
+        a, c, n = int(b.starts[i]), b.ctx[i], b.n[i]
         links = None if up is None else up[a:a + n]
         for e in range(4):
             # never the root: some row is left that does not see the node
-            t, h, dim, x = int(r.integers(1, n)), int(r.integers(H)), int(r.integers(D)), odd[e % 3]
+            t, h, dim, x = int(r.integers(1, n)), int(r.integers(b.H)), int(r.integers(b.D)), odd[e % 3]
             pos = c - n + t
-            at = (int(b.tables[i, pos // B]), h, pos % B, dim)
+            at = (int(b.tables[i, pos // b.B]), h, pos % b.B, dim)
             if e < 3:
                 b.v[at] = x
                 hit[a:a + n, h, dim] = True
@@ -75,6 +68,101 @@ def test_tree_attention_unseen_values_that_are_not_finite(D, B, n, chain):
     b.k, b.v = k, v
     b.check(torch.where(fine, got, clean).half(), up)
     assert bool(torch.isfinite(got[b.starts[:-1]]).all())     # the roots
+
+
+@pytest.mark.parametrize("D,B", [(64, 8), (64, 32), (128, 16)])
+@pytest.mark.parametrize("n", [2, 13, 32, 64])
+@pytest.mark.parametrize("chain", [False, True])
+def test_tree_attention_unseen_values_that_are_not_finite(D, B, n, chain):
+    """Contexts put the nodes in one tile of 128 positions, across two, and
+    behind a context in many parts."""
+    ctx = [n, 100 + n, 128 + n // 2, 256, 9000 + n]
+    b = Batch(D + n, ctx, [n] * len(ctx), 3, D, B, scale_q=2.0)
+    _plant_and_check(b, None if chain else b.forest(n), n, range(len(ctx)))
+
+
+def _mixed(seed, S, most_n, most_ctx):
+    r = np.random.default_rng(seed)
+    ctx = [int(c) for c in np.exp(r.uniform(0, math.log(most_ctx), S))]
+    return ctx, [int(r.integers(1, min(most_n, c) + 1)) for c in ctx]
+
+
+@pytest.mark.parametrize("D,B", [(64, 8), (64, 32), (128, 8), (128, 16), (128, 32)])
+@pytest.mark.parametrize("most_ctx", [60, 300, 2000])
+def test_many_units_of_few_rows(D, B, most_ctx):
+    """Batches that give every CTA several units of up to 16 rows, of one tile
+    and of several, and the same contexts with weights."""
+    ctx, n = _mixed(D + most_ctx, 61, 16, most_ctx)
+    b = Batch(D + B, ctx, n, 10, D, B, scale_q=2.0)
+    up = b.forest(2)
+    b.check(b.run(up), up)
+    b.check(b.run(None), None)
+    one = Batch(D + B, ctx, [1] * 61, 10, D, B, scale_q=2.0)
+    W = one.tables.shape[1] * B
+    w_in = torch.rand(61, 10, W, device="cuda")
+    st = _status()
+    out, w_out = _run_weights(one, w_in, W, status=st)
+    _check_weights(one, out, w_out, w_in, torch.full_like(w_out, -3.0))
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("D,B", [(64, 16), (128, 16)])
+@pytest.mark.parametrize("n", [1, 9, 16, 31, 64])
+@pytest.mark.parametrize("S", [2, 40])
+def test_scores_that_grow_along_the_context(D, B, n, S):
+    """Keys that raise a row's largest score by 12 in log2 units from tile to
+    tile, another row's in each, so what is summed so far is rescaled.  A score
+    of D products, fp32-accumulated, errs by at most e = D 2^-24 times the sum
+    of their sizes; a weight by that, and once more in the sum it is divided by.
+    2^(x - reference) enters the second product as fp16, which below 2^-14 has
+    steps of 2^-24: half of one, 2^-25, is its error there, and the sum it is
+    divided by is 1 or more, since a reference is the score of some position
+    seen (that one's term is 1 and a larger score's more).  A weight of 2^-14 or
+    more has a term of 2^-14 or more, so the rest add 2^-25 |v| each."""
+    H = 8
+    ctx = [600 + 17 * s for s in range(S)]
+    b = Batch(n + D, ctx, [n] * S, H, D, B)
+    up = b.forest(n)
+    scale2 = b.scale / math.log(2)
+    for s, c in enumerate(ctx):
+        a = int(b.starts[s])
+        for j, pos in enumerate((20, 140, 290, 420, 550)):
+            row = b.q[a + (3 * j) % n].float()                     # [H][D]
+            key = row * (12.0 * (j + 1) / (scale2 * (row * row).sum(-1, keepdim=True)))
+            b.k[int(b.tables[s, pos // B]), :, pos % B] = key.half()
+    out = b.run(up)
+    one = None
+    if n == 1:
+        one = _run_weights(b, None, b.tables.shape[1] * B)
+    for s, c in enumerate(ctx):
+        a = int(b.starts[s])
+        sees = torch.zeros(n, c, dtype=torch.bool)
+        sees[:, :c - n] = True
+        for t in range(n):
+            sees[t, [c - n + x for x in _sees(up[a:a + n], t)]] = True
+        q, k, v = b.q[a:a + n].double(), b.rows64(b.k, s), b.rows64(b.v, s)
+        x = torch.einsum("thd,phd->htp", q, k) * b.scale
+        w = torch.softmax(x.masked_fill(~sees.cuda(), -math.inf), -1)
+        e = D * 2.0 ** -24 * float(torch.einsum("thd,phd->htp", q.abs(), k.abs()).max()) * b.scale
+        ref = torch.einsum("htp,phd->thd", w, v)
+        size = torch.einsum("htp,phd->thd", w, v.abs())
+        small = (sees.cuda() & (w < 2.0 ** -14)).double()
+        steps = 2.0 ** -25 * torch.einsum("htp,phd->thd", small, v.abs())
+        tol = 2.0 ** -11 * ref.abs() + (2.0 ** -11 + 2 * e) * size + steps + 2.0 ** -24
+        err = (out[a:a + n].double() - ref).abs()
+        assert bool((err <= tol).all()), (s, float((err - tol).max()))
+        if one is not None:
+            got = one[1][s, :, :c].double()
+            assert bool(((got - w[:, 0]).abs() <= (2 * e + 2.0 ** -23) * w[:, 0] + 1e-30).all())
+
+
+@pytest.mark.parametrize("D,B", [(64, 8), (128, 16)])
+def test_many_units_with_values_that_are_not_finite(D, B):
+    ctx, n = _mixed(D, 61, 16, 700)
+    n = [max(2, k) for k in n]
+    ctx = [max(c, k) for c, k in zip(ctx, n)]
+    b = Batch(D + 1, ctx, n, 10, D, B, scale_q=2.0)
+    _plant_and_check(b, b.forest(4), 4, range(0, 61, 3))
 
 
 def test_tree_attention_rows_with_infinite_scores_leave_the_others():
