@@ -31,8 +31,8 @@ constexpr unsigned kAll = 0xffffffffu;
 // by the barriers between these steps, so short rows take small CTAs, several
 // an SM.
 //
-// Measured: 64 sequences of 256 to 2048 positions x 40 heads, 512 kept: 26 us (11 MB
-// read: 2 us; with the move 214 us, and 237 with 1024 threads a CTA instead of
+// Measured: 64 sequences of 256 to 2048 positions x 40 heads, 512 kept: 24 us (11 MB
+// read: 2 us; with the move 212 us, and 237 with 1024 threads a CTA instead of
 // 256, 223 with more histograms instead of ranking).  4 of 20 to 32 thousand, 4096
 // kept: some 45 us, the move 110 (with more histograms 4 us later; a row in
 // shared memory, which leaves one CTA an SM above kCached, 1 us earlier).
@@ -58,8 +58,10 @@ struct SelectParams {
     int32_t *status;
 };
 
+// (Six small CTAs an SM, which 42 registers allow: 212 us with the move for 64
+// sequences, 214 with the 63 that the compiler takes otherwise.)
 template <bool CACHED, int kSelThreads>
-__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectParams a) {
+__global__ void __launch_bounds__(kSelThreads, kSelThreads == 256 ? 6 : 2) evict_select_kernel(const SelectParams a) {
     constexpr int kSelWarps = kSelThreads / 32;
     extern __shared__ float row_sh[];
     __shared__ __align__(16) uint32_t bins[kBins];   // after a histogram: the few keys of the bin
