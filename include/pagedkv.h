@@ -534,6 +534,9 @@ int pa_prefill_step_attention(void *out, const void *q, const void *k_new, const
  * 8, 16 or 32, n_seqs <= PA_TREE_MAX_SEQS.  How long contexts are cut into
  * parts depends on the whole batch, so a sequence's result agrees between
  * batches to rounding, not to the bit; it does not depend on where blocks are.
+ * Sums are fp32; a row's weights meet the values as fp16 numbers, an error of
+ * 2^-11 of a weight at most, and for weights below 2^-21 of the row's largest one
+ * of 2^-32 of that (pa_decode_attention keeps them in fp32).
  * Slots past ctx are never used, and what a row does not see never changes it,
  * not where keys or values there are infinite or NaN (the head of that sequence
  * then takes longer).  Reported in *status: PA_ERR_INVALID_ARG for

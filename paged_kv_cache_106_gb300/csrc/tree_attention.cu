@@ -40,13 +40,20 @@
 //     945 -> 779 us; at 16 rows 8 gave 22.4 instead of 21.9 us for one sequence,
 //     247 instead of 246 us for 64).  Up to 16 rows and with two units a CTA or
 //     more there are two groups of 4 that take units in turn (launch_tree).
-// Scores are taken relative to a reference per row that only moves where a
-// score passes it by 2^8 (then O and the sums are rescaled; P stays below 2^8 in
-// fp16): almost every tile goes without a reduction over its tokens.
+// Scores are taken relative to a reference per row, 7 binary orders below the
+// largest score when it is set, that only moves where a score passes it by 15
+// (then O and the sums are rescaled): almost every tile goes without a reduction
+// over its tokens.
 //
-// Rounding: products of fp16 values are exact in the fp32 accumulators; P enters
-// the second product as fp16 (half a unit in 2^-11 of each weight, like the fp16
-// output's own rounding); sums, references and the join of parts are fp32.
+// Rounding: products of fp16 values are exact in the fp32 accumulators; sums,
+// references and the join of parts are fp32.  P enters the second product as fp16,
+// which is what the tensor cores take beside fp16 values: 2^-11 of each weight at
+// most, like the fp16 output's own rounding.  Below 2^-14 fp16 has steps of 2^-24,
+// so the references lie where P uses its upper bits: the largest term of a row is
+// 2^7 to 2^15, and only weights below 2^-21 of the largest one meet those steps
+// (half of one is 2^-32 of the largest weight).  With references at the maximum a
+// first position of 20 binary orders above 32 thousand others, its own value 0,
+// left the output off by 3 % (now 2^-11).
 //
 // Work plan (the same in every CTA, no counters to clear): sequences are cut into
 // even parts by part_size; cut ones first, then the others by size, dealt to the
@@ -95,7 +102,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHeaderBytes = 256;    // workspace head: number of cut sequences
 constexpr int kUnitSlots = 8;        // units a CTA has open (with 3, 256 sequences of 100 positions took 164 instead of 161 us)
 constexpr int kTile = 128;           // tokens of a tile: the lanes of tensor memory
-constexpr float kRescaleLog2 = 8.f;  // tensor-memory kernel: how far a row's maximum may pass its reference
+constexpr float kBelowLog2 = 7.f;    // how far below its row's largest score a reference is set
+constexpr float kRescaleLog2 = 15.f; // how far scores may pass it: P stays in fp16's range
 
 struct TreeParams {
     __half *out;
@@ -1081,7 +1089,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ, G>::THREADS), 1)
                     }
                 };
                 scores();
-                // a row's reference moves when a score passes it by more than 2^8
+                // a row's reference moves when a score passes it by more than 2^15
                 bool over = false;
                 if (t0 > 0) {
                     float top = -INFINITY;
@@ -1111,7 +1119,7 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ, G>::THREADS), 1)
                         const float top = fmaxf(fmaxf(red[id], red[NQ + id]), fmaxf(red[2 * NQ + id], red[3 * NQ + id]));
                         // (a row that has seen nothing yet has reference -2^100: its
                         // terms, if any come, are rescaled from 0)
-                        const float old = t0 ? ref[id] : -0x1p100f, now = top > old + kRescaleLog2 ? top : old;
+                        const float old = t0 ? ref[id] : -0x1p100f, now = top > old + kRescaleLog2 ? top - kBelowLog2 : old;
                         ref[id] = now;
                         corr[id] = ex2(old - now);
                     }
