@@ -537,9 +537,12 @@ int pa_prefill_step_attention(void *out, const void *q, const void *k_new, const
  * Sums are fp32; a row's weights meet the values as fp16 numbers, an error of
  * 2^-11 of a weight at most, and for weights below 2^-21 of the row's largest one
  * of 2^-32 of that (pa_decode_attention keeps them in fp32).
- * Slots past ctx are never used, and what a row does not see never changes it,
- * not where keys or values there are infinite or NaN (the head of that sequence
- * then takes longer).  Reported in *status: PA_ERR_INVALID_ARG for
+ * Slots past ctx are never used, and what a row does not see does not change it:
+ * not a bit for finite keys and values and for keys that are infinite or NaN.
+ * Where a node's value is not finite, the rows that do not see it are added up
+ * once more in that dimension without it, with fp32 weights and in another
+ * order, so they agree to rounding there (and the head of that sequence takes
+ * longer).  Reported in *status: PA_ERR_INVALID_ARG for
  * n < 0, n > ctx, n > max_q_len or rows outside [0, q_rows) (that sequence is
  * left unwritten), and for a parent that is no earlier node (taken as -1);
  * PA_ERR_BAD_BLOCK for ctx > max_blocks * B (left unwritten) or a table entry

@@ -1071,27 +1071,32 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ, G>::THREADS), 1)
                     wait(bar_seen + 8 * slot, (k / kUnitSlots) & 1u);
                     knows = true;
                 }
-                // the tile's scores less the references, -inf where the row does not see
-                float y[CQ];
-                auto scores = [&]() {
-                    load_cols(Cfg::S_COL + b * NQ, y);
-                    if (SCORES && tok < nv)
-                        p.scores[((size_t)s * H + h) * p.score_stride + pos] = y[0] * qs;
-#pragma unroll
-                    for (int i = 0; i < R; ++i) y[i] = fmaf(y[i], qs, off[i]);
+                // -inf where the row does not see this position
+                auto hide = [&](auto &x) {
                     if (tok_first + t0 + kTile > base || nv < kTile) {
-                        // who sees this position: every row before the nodes, then
-                        // the node itself and its descendants; none past the end
+                        // who sees it: every row before the nodes, then the node
+                        // itself and its descendants; none past the end
                         const uint64_t v = (tok >= nv ? 0ull : pos < base ? ~0ull : seen[slot * NQ + pos - base]) >> col0;
 #pragma unroll
                         for (int i = 0; i < R; ++i)
-                            if (!((v >> i) & 1)) y[i] = -INFINITY;
+                            if (!((v >> i) & 1)) x[i] = -INFINITY;
                     }
                 };
-                scores();
+                // the tile's products, then its scores less the references (by
+                // one rounding on every way here, so that a row does not depend
+                // on whether another's reference moves)
+                float y[CQ];
+                auto scores = [&]() {
+#pragma unroll
+                    for (int i = 0; i < R; ++i) y[i] = fmaf(y[i], qs, off[i]);
+                    hide(y);
+                };
+                load_cols(Cfg::S_COL + b * NQ, y);
+                if (SCORES && tok < nv) p.scores[((size_t)s * H + h) * p.score_stride + pos] = y[0] * qs;
                 // a row's reference moves when a score passes it by more than 2^15
                 bool over = false;
                 if (t0 > 0) {
+                    scores();
                     float top = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < R; c += 8)
@@ -1103,14 +1108,11 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ, G>::THREADS), 1)
                 }
                 if (t0 == 0 || softmax_any<ST>(group, over || !ok)) {
                     if (!softmax_all<ST>(group, ok)) break;
-                    if (t0 > 0) {                        // the scores themselves
+                    if (t0 > 0) load_cols(Cfg::S_COL + b * NQ, y);
+                    float m[R];                          // the scores themselves
 #pragma unroll
-                        for (int i = 0; i < R; ++i) off[i] = 0.f;
-                        scores();
-                    }
-                    float m[R];
-#pragma unroll
-                    for (int i = 0; i < R; ++i) m[i] = y[i];
+                    for (int i = 0; i < R; ++i) m[i] = y[i] * qs;
+                    hide(m);
                     const int first = warp_combine(m, lane, [](float a, float c) { return fmaxf(a, c); });
 #pragma unroll
                     for (int i = 0; i < (R + 31) / 32; ++i) red[(warp & 3) * NQ + col0 + first + i] = m[i];
@@ -1118,10 +1120,12 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ, G>::THREADS), 1)
                     if (id < (SCORES ? 1 : NQ)) {
                         const float top = fmaxf(fmaxf(red[id], red[NQ + id]), fmaxf(red[2 * NQ + id], red[3 * NQ + id]));
                         // (a row that has seen nothing yet has reference -2^100: its
-                        // terms, if any come, are rescaled from 0)
+                        // terms, if any come, are rescaled from 0; a column that
+                        // is no row, and holds the next sequence's scores, has no
+                        // terms and never moves)
                         const float old = t0 ? ref[id] : -0x1p100f, now = top > old + kRescaleLog2 ? top - kBelowLog2 : old;
-                        ref[id] = now;
-                        corr[id] = ex2(old - now);
+                        ref[id] = id < n ? now : INFINITY;
+                        corr[id] = id < n ? ex2(old - now) : 0.f;
                     }
                     softmax_sync<ST>(group);
 #pragma unroll
@@ -1152,12 +1156,8 @@ __global__ void __launch_bounds__((TreeCfg<D, NQ, G>::THREADS), 1)
                     // (32 rows a thread do not stay in registers up to here: spilled
                     // they cost more than the second load, 785 instead of 771 us
                     // for 256 sequences of 64 nodes)
-                    if constexpr (R <= 16) {
-#pragma unroll
-                        for (int i = 0; i < R; ++i) y[i] += off[i];
-                    } else {
-                        scores();
-                    }
+                    if constexpr (R > 16) load_cols(Cfg::S_COL + b * NQ, y);
+                    scores();
                 }
                 // P of the tile: this token's row, in the second operand's layout
                 uint32_t w[(R + 7) / 8 * 4];

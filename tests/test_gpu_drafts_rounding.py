@@ -98,3 +98,52 @@ def test_weights_beside_a_dominant_position(D, gap):
     x = q[0, 0, 0].double() * k[0, 0, 0, 0].double() * scale
     one = torch.exp(-x) / (1 + (ctx - 1) * torch.exp(-x))
     assert bool(((w[0, :, 1:].double() - one).abs() <= (2.0 ** -17 + ctx / 128 * 2.0 ** -24) * one).all())
+
+
+# ------------------------------------------- rows beside rows that jump
+
+
+@pytest.mark.parametrize("D,B", [(64, 16), (128, 16)])
+@pytest.mark.parametrize("n,S", [(7, 24), (16, 24), (16, 90), (30, 24), (64, 24)])
+def test_tree_attention_rows_do_not_depend_on_keys_they_do_not_see(D, B, n, S):
+    """A node whose finite key lifts the scores of the rows that see it by some
+    20 binary orders: every other row is the same to the bit."""
+    H = 8
+    ctx = [300 + 7 * s for s in range(S)]
+    b = Batch(n + D + S, ctx, [n] * S, H, D, B, scale_q=2.0)
+    up = b.forest(n)
+    clean = b.run(up)
+    seen = torch.zeros(b.rows + 2, dtype=torch.bool, device="cuda")
+    r = np.random.default_rng(n)
+    for s, c in enumerate(ctx):
+        a, t = int(b.starts[s]), int(r.integers(1, n))
+        row = b.q[a + t].float()
+        key = row * (20.0 * math.log(2) / (b.scale * (row * row).sum(-1, keepdim=True)))
+        pos = c - n + t
+        b.k[int(b.tables[s, pos // B]), :, pos % B] = key.half()
+        for x in range(t, n):
+            y = x
+            while y > t:
+                y = int(up[a + y])
+            seen[a + x] = y == t
+    assert bool(seen.any())
+    got = b.run(up)
+    assert torch.equal(got[~seen], clean[~seen])
+    # (the scores' error, D 2^-24 of the sum of |q k| <= 20 binary orders and some,
+    # stays below the 2^-12 that the check allows)
+    b.check(got, up)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 5, 13, 21])
+def test_tree_attention_does_not_depend_on_the_next_sequence(D, n):
+    """Rows are handled by eight: those of the next sequence among them, whose
+    queries here are large."""
+    S, H = 40, 8
+    b = Batch(n + D, [500 + 9 * s for s in range(S)], [n] * S, H, D, 16)
+    up = b.forest(n)
+    clean = b.run(up)
+    odd = torch.arange(b.rows, device="cuda") // n % 2 == 1
+    b.q[:b.rows][odd] = b.q[:b.rows][odd] * 40
+    got = b.run(up)
+    assert torch.equal(got[:b.rows][~odd], clean[:b.rows][~odd])
