@@ -407,12 +407,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const Ve
             // lane l: the sums of warps kPerLane l .. of the row
             const Pair zero = {0.f, 0.f};
             Pair run[kPerLane];
+            bool weighs[kPerLane];
             int positive = -1;
 #pragma unroll
             for (int e = 0; e < kPerLane; ++e) {
                 const int w = kPerLane * lane + e;
                 const Pair v = w < (int)C * kWarps ? sh.sums[parity][w] : zero;
-                if (v.hi > 0.f) positive = w;
+                weighs[e] = v.hi > 0.f;
+                if (weighs[e]) positive = w;
                 run[e] = e ? add(run[e - 1], v) : v;
             }
             const Pair incl = scan(run[kPerLane - 1]), total = from_lane(incl, 31);
@@ -429,13 +431,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const Ve
             } else {
                 // the warp whose span the target falls into finds the token; the
                 // last one with any weight where the target rounds to the total
+                // (the sums before a span are added up in another order than those
+                // up to the span before it, so a target on the border of two can
+                // seem to lie between them: in no span without weight)
                 const Pair target = times(us, 1.f, total);
                 Pair before = {__shfl_up_sync(kAll, incl.hi, 1), __shfl_up_sync(kAll, incl.lo, 1)}, from = zero;
                 if (lane == 0) before = zero;
                 int mine = INT_MAX;
 #pragma unroll
                 for (int e = kPerLane - 1; e >= 0; --e) {
-                    if (above(add(before, run[e]), target)) {
+                    if (weighs[e] && above(add(before, run[e]), target)) {
                         mine = kPerLane * lane + e;
                         from = e ? add(before, run[e > 0 ? e - 1 : 0]) : before;
                     }
@@ -478,14 +483,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draft_kernel(const Ve
                 for (int b = 0; b < kRound; ++b) t[b] = over_lanes(t[b]);
 #pragma unroll
                 for (int b = 0; b < kRound; ++b) {
-                    if (t[b].hi > 0.f && !above(base, left)) {
+                    // (the first one of any weight even where `base` seems past it)
+                    if (t[b].hi > 0.f && (in < 0 || !above(base, left))) {
                         in = j + b;
                         before = base;
                     }
                     base = add(base, t[b]);
                 }
             }
-            const int x = lo + max(in, 0) * 128 - row.shift;
+            const int x = lo + in * 128 - row.shift;
             float4 qv = make_float4(0.f, 0.f, 0.f, 0.f);
             const float4 pv = edge4(row.p, x, V);
             if (DRAFT && row.k > 0) qv = edge4(row.q, x, V);

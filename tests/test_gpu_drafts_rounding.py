@@ -147,3 +147,34 @@ def test_tree_attention_does_not_depend_on_the_next_sequence(D, n):
     b.q[:b.rows][odd] = b.q[:b.rows][odd] * 40
     got = b.run(up)
     assert torch.equal(got[:b.rows][~odd], clean[:b.rows][~odd])
+
+
+# ------------------------------------------------- verification's borders
+
+
+@pytest.mark.parametrize("V,front,back,S", [(1020, 768, 1000, 4096), (20476, 1536, 2053, 1000)])
+def test_verify_random_numbers_on_a_border(V, front, back, S):
+    """u_sample = 1/2 falls, to the rounding of the sums, on the border between
+    the tokens before `front` and two at `back` that weigh as much together;
+    nothing between them weighs anything.  The next token is the last one before
+    the border or the first one behind it."""
+    r = np.random.default_rng(V)
+    p = np.zeros((S, V), np.float32)
+    # over so many binary orders that sums in another order round otherwise
+    p[:, :front] = np.exp2(-24 * r.random((S, front))) / front
+    for s in range(S):
+        total = math.fsum(p[s, :front].tolist())
+        hi = np.float32(total)
+        if float(hi) >= total:
+            hi = np.nextafter(hi, np.float32(0))
+        p[s, back], p[s, back + 1] = hi, np.float32(total - float(hi))
+    assert (p[:, [front - 1, back, back + 1]] > 0).all()
+    st = _status()
+    starts = np.arange(S + 1)
+    path, lens, nxt = _verify(_dev(p), None, np.zeros(S), None, starts, np.zeros(S), np.full(S, 0.5), status=st)
+    assert st.item() == 0
+    assert np.isin(nxt, [front - 1, back]).all(), np.unique(nxt[~np.isin(nxt, [front - 1, back])])
+    # beside the border there is no doubt
+    for us, want in ((0.5 - 2.0 ** -12, range(front)), (0.5 + 2.0 ** -12, [back])):
+        _, _, nxt = _verify(_dev(p), None, np.zeros(S), None, starts, np.zeros(S), np.full(S, us), status=st)
+        assert np.isin(nxt, list(want)).all()
