@@ -646,7 +646,8 @@ int pa_evict_select(int32_t *keep, int32_t *keep_lens, float *weights_out, const
  * be src_tables, or hold, entry by entry, either the same block or one that
  * src_tables does not hold anywhere in the call (pa_seq_compact's).  Two
  * sequences must not write one block.
- *   k_caches, v_caches  (host) arrays of num_layers (<= 128) device pointers
+ *   k_caches, v_caches  (host) arrays of num_layers (<= 128) device pointers, to
+ *                 caches that do not overlap
  *   src_tables, dst_tables  [n_seqs][max_blocks] int32
  *   src_lens      [n_seqs] int32: positions the sequence holds before the move
  *   first         [n_seqs] int32, or NULL for 0

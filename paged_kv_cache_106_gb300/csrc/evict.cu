@@ -471,6 +471,13 @@ int launch_compact_kv(void *const *k_caches, void *const *v_caches, int32_t num_
         a.cache[2 * l] = static_cast<uint4 *>(k_caches[l]);
         a.cache[2 * l + 1] = static_cast<uint4 *>(v_caches[l]);
     }
+    // CTAs of their own move each cache, so none may be there twice
+    uintptr_t at[2 * kMaxMoveLayers];
+    const uintptr_t bytes = (uintptr_t)d->num_blocks * d->num_heads * d->block_size * d->head_dim * 2;
+    for (int i = 0; i < 2 * num_layers; ++i) at[i] = reinterpret_cast<uintptr_t>(a.cache[i]);
+    std::sort(at, at + 2 * num_layers);
+    for (int i = 1; i < 2 * num_layers; ++i)
+        if (at[i] - at[i - 1] < bytes) return fail(PA_ERR_INVALID_ARG, "%s: caches overlap", who);
     a.src_tables = src_tables;
     a.dst_tables = dst_tables;
     a.src_lens = src_lens;
