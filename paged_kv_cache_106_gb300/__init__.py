@@ -148,11 +148,13 @@ def _check(rc: int):
 
 
 def _need_elems(n_elems: int, **tensors):
-    """Refuses a tensor holding fewer elements than the call reads from it
-    (None is left to the library, which refuses a NULL it needs; a raw address
-    has no length to check)."""
+    """Refuses a tensor holding fewer elements than the call reads from it, and
+    a raw address, whose length is not known (None is left to the library, which
+    refuses a NULL it needs)."""
     for name, t in tensors.items():
-        if t is not None and not isinstance(t, int) and t.numel() < n_elems:
+        if isinstance(t, int):
+            raise ValueError(f"{name} is an address, a tensor of {n_elems} elements is read")
+        if t is not None and t.numel() < n_elems:
             raise ValueError(f"{name} holds {t.numel()} elements, the call reads {n_elems}")
 
 

@@ -1,8 +1,10 @@
-"""Arguments of the calls for drafted tokens and for the bounded cache that are
-refused, or taken, on the host (none of these addresses is ever read)."""
+"""Arguments of the calls for drafted tokens, for the bounded cache and of the
+one-call steps that are refused, or taken, on the host (none of these addresses
+is ever read)."""
 import ctypes
 
 import pytest
+import torch
 
 import paged_kv_cache_106_gb300 as pk
 
@@ -26,3 +28,15 @@ def test_moves_refuse_caches_that_overlap(k, v):
     rows would be read after they were written over."""
     assert _compact(k, v) == pk.PA_ERR_INVALID_ARG
     assert "overlap" in pk.pa_last_error_string()
+
+
+def test_one_call_steps_refuse_addresses_of_new_rows():
+    """How many rows lie there cannot be checked."""
+    q, tables, ctx = torch.zeros(3, 2, 64), torch.zeros(3, 4), torch.zeros(3)
+    slots = torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="k_new"):
+        pk.pa_decode_step_attention(q, q, A, q, slots, q, q, tables, ctx, 0.1, DESC)
+    with pytest.raises(ValueError, match="slot_mapping"):
+        pk.pa_decode_step_attention(q, q, q, q, A, q, q, tables, ctx, 0.1, DESC)
+    with pytest.raises(ValueError, match="v_new"):
+        pk.pa_prefill_step_attention(q, q, q, A, q, q, tables, ctx, ctx, 0.1, DESC, max_q_len=3)
