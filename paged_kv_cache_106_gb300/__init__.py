@@ -590,7 +590,16 @@ def _raw_stream(torch, stream):
 
 
 def _workspace(ws):
-    return 0 if ws is None else ws.numel() * ws.element_size()
+    """Device address and bytes of a contiguous CUDA tensor of any type (None is
+    left to the library, which refuses it)."""
+    if ws is None:
+        return None, 0
+    if ws.__class__ is int:
+        raise ValueError("workspace: an address, whose size is not known")
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError(f"workspace: a contiguous CUDA tensor is used, not {tuple(ws.shape)} on "
+                         f"{ws.device}{'' if ws.is_contiguous() else ', not contiguous'}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def pa_tree_workspace_bytes(n_seqs: int, max_blocks: int, max_q_len: int, desc: PoolDesc) -> int:
@@ -617,7 +626,7 @@ def pa_tree_attention(out, q, k_cache, v_cache, block_tables, ctx_lens, q_starts
         _arg("k_cache", k_cache, f16, cache), _arg("v_cache", v_cache, f16, cache),
         _arg("block_tables", block_tables, i32, n * mb), _arg("ctx_lens", ctx_lens, i32, n),
         _arg("q_starts", q_starts, i32, n + 1), _arg("parents", parents, i32, rows), n, mb,
-        max_q_len, rows, scale, _dev(workspace), _workspace(workspace), _arg("status", status, i32, 1),
+        max_q_len, rows, scale, *_workspace(workspace), _arg("status", status, i32, 1),
         desc.ref, _raw_stream(torch, stream)))
 
 
@@ -680,7 +689,7 @@ def pa_decode_attention_weights(out, weights_out, weights_in, q, k_cache, v_cach
         _arg("weights_in", weights_in, f32, sums), wl, _arg("q", q, f16, n * width),
         _arg("k_cache", k_cache, f16, cache), _arg("v_cache", v_cache, f16, cache),
         _arg("block_tables", block_tables, i32, n * mb), _arg("ctx_lens", ctx_lens, i32, n), n, mb,
-        scale, _dev(workspace), _workspace(workspace), _arg("status", status, i32, 1), desc.ref,
+        scale, *_workspace(workspace), _arg("status", status, i32, 1), desc.ref,
         _raw_stream(torch, stream)))
 
 

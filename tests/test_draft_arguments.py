@@ -40,3 +40,68 @@ def test_one_call_steps_refuse_addresses_of_new_rows():
         pk.pa_decode_step_attention(q, q, q, q, A, q, q, tables, ctx, 0.1, DESC)
     with pytest.raises(ValueError, match="v_new"):
         pk.pa_prefill_step_attention(q, q, q, A, q, q, tables, ctx, ctx, 0.1, DESC, max_q_len=3)
+
+
+class Fake:
+    """What the bindings ask of a tensor; the calls here end before its address
+    is used (scale is NaN, which the library refuses, where nothing else is)."""
+
+    def __init__(self, shape, dtype=torch.float16, device=0, contiguous=True):
+        self.shape, self.dtype, self.contiguous = shape, dtype, contiguous
+        self.device = torch.device("cuda", device) if device >= 0 else torch.device("cpu")
+        self.is_cuda, self.index = device >= 0, device
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def numel(self):
+        return int(torch.Size(self.shape).numel())
+
+    def element_size(self):
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def data_ptr(self):
+        return A
+
+
+def _i32(*shape, **kw):
+    return Fake(shape, torch.int32, **kw)
+
+
+def _tree(**changed):
+    a = dict(out=Fake((4, 2, 64)), q=Fake((4, 2, 64)), k_cache=Fake((8, 2, 16, 64)),
+             v_cache=Fake((8, 2, 16, 64)), block_tables=_i32(2, 4), ctx_lens=_i32(2),
+             q_starts=_i32(3), parents=_i32(4), scale=float("nan"), desc=DESC, max_q_len=4,
+             workspace=Fake((1 << 30,), torch.uint8), stream=0)
+    pk.pa_tree_attention(**{**a, **changed})
+
+
+def _weights(**changed):
+    a = dict(out=Fake((2, 2, 64)), weights_out=Fake((2, 2, 64), torch.float32), weights_in=None,
+             q=Fake((2, 2, 64)), k_cache=Fake((8, 2, 16, 64)), v_cache=Fake((8, 2, 16, 64)),
+             block_tables=_i32(2, 4), ctx_lens=_i32(2), scale=float("nan"), desc=DESC,
+             workspace=Fake((1 << 30,), torch.uint8), stream=0)
+    pk.pa_decode_attention_weights(**{**a, **changed})
+
+
+@pytest.fixture
+def one_gpu(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+
+@pytest.mark.parametrize("call", [_tree, _weights])
+def test_workspaces_are_checked(call, one_gpu):
+    with pytest.raises(pk.PagedKVError, match="scale"):      # nothing else is wrong
+        call()
+    for bad in (A, Fake((1 << 20,), torch.uint8, device=-1), Fake((1 << 20,), contiguous=False)):
+        with pytest.raises(ValueError, match="workspace"):
+            call(workspace=bad)
+    # any type will do; none is refused by the library
+    with pytest.raises(pk.PagedKVError, match="scale"):
+        call(workspace=Fake((1 << 20,), torch.float32))
+    with pytest.raises(pk.PagedKVError, match="workspace"):
+        call(workspace=None, scale=0.1)
