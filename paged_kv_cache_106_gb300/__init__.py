@@ -571,14 +571,20 @@ def _load_torch():
     return torch
 
 
-def _arg(name, t, dtype, n):
-    """Device address of a contiguous CUDA tensor of dtype with n elements or
-    more (a raw address or None as it is)."""
+def _here(torch):
+    """Index of the current GPU, where the calls' kernels run (before CUDA is in
+    use: -2, no tensor's)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _arg(name, t, dtype, n, here):
+    """Device address of a contiguous tensor of dtype on the current GPU with n
+    elements or more (a raw address or None as it is)."""
     if t is None or t.__class__ is int:
         return t
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{name}: a contiguous CUDA tensor of {n} or more {dtype} is read, "
-                         f"not {tuple(t.shape)} {t.dtype} on {t.device}"
+    if t.dtype is not dtype or t.get_device() != here or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: a contiguous tensor of {n} or more {dtype} on the current GPU "
+                         f"is read, not {tuple(t.shape)} {t.dtype} on {t.device}"
                          f"{'' if t.is_contiguous() else ', not contiguous'}")
     return t.data_ptr()
 
@@ -589,16 +595,17 @@ def _raw_stream(torch, stream):
     return stream if stream.__class__ is int else stream.cuda_stream
 
 
-def _workspace(ws):
-    """Device address and bytes of a contiguous CUDA tensor of any type (None is
-    left to the library, which refuses it)."""
+def _workspace(ws, here):
+    """Device address and bytes of a contiguous tensor of any type on the current
+    GPU (None is left to the library, which refuses it)."""
     if ws is None:
         return None, 0
     if ws.__class__ is int:
         raise ValueError("workspace: an address, whose size is not known")
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError(f"workspace: a contiguous CUDA tensor is used, not {tuple(ws.shape)} on "
-                         f"{ws.device}{'' if ws.is_contiguous() else ', not contiguous'}")
+    if ws.get_device() != here or not ws.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on the current GPU is used, not "
+                         f"{tuple(ws.shape)} on {ws.device}"
+                         f"{'' if ws.is_contiguous() else ', not contiguous'}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -614,6 +621,7 @@ def pa_tree_attention(out, q, k_cache, v_cache, block_tables, ctx_lens, q_starts
     the last positions of sequence s, each seeing the positions before the
     nodes, itself and its ancestors by ``parents`` (None: a chain)."""
     torch = _torch or _load_torch()
+    here = _here(torch)
     f16, i32 = torch.float16, torch.int32
     n = ctx_lens.shape[0] if n_seqs is None else int(n_seqs)
     mb = block_tables.shape[1] if max_blocks is None else int(max_blocks)
@@ -622,12 +630,13 @@ def pa_tree_attention(out, q, k_cache, v_cache, block_tables, ctx_lens, q_starts
     width = c.num_heads * c.head_dim
     cache = c.num_blocks * c.block_size * width
     _check(_lib.pa_tree_attention(
-        _arg("out", out, f16, rows * width), _arg("q", q, f16, rows * width),
-        _arg("k_cache", k_cache, f16, cache), _arg("v_cache", v_cache, f16, cache),
-        _arg("block_tables", block_tables, i32, n * mb), _arg("ctx_lens", ctx_lens, i32, n),
-        _arg("q_starts", q_starts, i32, n + 1), _arg("parents", parents, i32, rows), n, mb,
-        max_q_len, rows, scale, *_workspace(workspace), _arg("status", status, i32, 1),
-        desc.ref, _raw_stream(torch, stream)))
+        _arg("out", out, f16, rows * width, here), _arg("q", q, f16, rows * width, here),
+        _arg("k_cache", k_cache, f16, cache, here), _arg("v_cache", v_cache, f16, cache, here),
+        _arg("block_tables", block_tables, i32, n * mb, here),
+        _arg("ctx_lens", ctx_lens, i32, n, here), _arg("q_starts", q_starts, i32, n + 1, here),
+        _arg("parents", parents, i32, rows, here), n, mb, max_q_len, rows, scale,
+        *_workspace(workspace, here), _arg("status", status, i32, 1, here), desc.ref,
+        _raw_stream(torch, stream)))
 
 
 def pa_verify_draft(path, path_lens, next_tokens, target_probs, draft_probs, draft_tokens,
@@ -638,6 +647,7 @@ def pa_verify_draft(path, path_lens, next_tokens, target_probs, draft_probs, dra
     bfloat16; draft_probs None: tokens picked outright) and given uniform
     numbers.  ``path`` is int32 [n_seqs, max_q_len]."""
     torch = _torch or _load_torch()
+    here = _here(torch)
     f32, i32 = torch.float32, torch.int32
     n = u_sample.shape[0] if n_seqs is None else int(n_seqs)
     mq = path.shape[1] if max_q_len is None else int(max_q_len)
@@ -652,13 +662,14 @@ def pa_verify_draft(path, path_lens, next_tokens, target_probs, draft_probs, dra
     if path.shape[1] != mq:
         raise ValueError(f"path is {path.shape[1]} wide, max_q_len {mq}")
     _check(_lib.pa_verify_draft(
-        _arg("path", path, i32, n * mq), _arg("path_lens", path_lens, i32, n),
-        _arg("next_tokens", next_tokens, i32, n), _arg("target_probs", target_probs, kind, 0),
-        _arg("draft_probs", draft_probs, kind, rows * vocab), code,
-        _arg("draft_tokens", draft_tokens, i32, rows), _arg("parents", parents, i32, rows),
-        _arg("q_starts", q_starts, i32, n + 1), _arg("u_accept", u_accept, f32, rows),
-        _arg("u_sample", u_sample, f32, n), n, mq, rows, vocab, _arg("status", status, i32, 1),
-        _raw_stream(torch, stream)))
+        _arg("path", path, i32, n * mq, here), _arg("path_lens", path_lens, i32, n, here),
+        _arg("next_tokens", next_tokens, i32, n, here),
+        _arg("target_probs", target_probs, kind, 0, here),
+        _arg("draft_probs", draft_probs, kind, rows * vocab, here), code,
+        _arg("draft_tokens", draft_tokens, i32, rows, here),
+        _arg("parents", parents, i32, rows, here), _arg("q_starts", q_starts, i32, n + 1, here),
+        _arg("u_accept", u_accept, f32, rows, here), _arg("u_sample", u_sample, f32, n, here), n,
+        mq, rows, vocab, _arg("status", status, i32, 1, here), _raw_stream(torch, stream)))
 
 
 def pa_decode_weights_workspace_bytes(n_seqs: int, max_blocks: int, desc: PoolDesc) -> int:
@@ -673,6 +684,7 @@ def pa_decode_attention_weights(out, weights_out, weights_in, q, k_cache, v_cach
     (float32 [n_seqs, num_heads, weight_len], None: zeros) into weights_out,
     which may be the same tensor."""
     torch = _torch or _load_torch()
+    here = _here(torch)
     f16, f32, i32 = torch.float16, torch.float32, torch.int32
     n = q.shape[0] if n_seqs is None else int(n_seqs)
     mb = block_tables.shape[1] if max_blocks is None else int(max_blocks)
@@ -685,12 +697,12 @@ def pa_decode_attention_weights(out, weights_out, weights_in, q, k_cache, v_cach
     width = c.num_heads * c.head_dim
     cache, sums = c.num_blocks * c.block_size * width, n * c.num_heads * wl
     _check(_lib.pa_decode_attention_weights(
-        _arg("out", out, f16, n * width), _arg("weights_out", weights_out, f32, sums),
-        _arg("weights_in", weights_in, f32, sums), wl, _arg("q", q, f16, n * width),
-        _arg("k_cache", k_cache, f16, cache), _arg("v_cache", v_cache, f16, cache),
-        _arg("block_tables", block_tables, i32, n * mb), _arg("ctx_lens", ctx_lens, i32, n), n, mb,
-        scale, *_workspace(workspace), _arg("status", status, i32, 1), desc.ref,
-        _raw_stream(torch, stream)))
+        _arg("out", out, f16, n * width, here), _arg("weights_out", weights_out, f32, sums, here),
+        _arg("weights_in", weights_in, f32, sums, here), wl, _arg("q", q, f16, n * width, here),
+        _arg("k_cache", k_cache, f16, cache, here), _arg("v_cache", v_cache, f16, cache, here),
+        _arg("block_tables", block_tables, i32, n * mb, here),
+        _arg("ctx_lens", ctx_lens, i32, n, here), n, mb, scale, *_workspace(workspace, here),
+        _arg("status", status, i32, 1, here), desc.ref, _raw_stream(torch, stream)))
 
 
 def pa_evict_select(keep, keep_lens, weights_out, weights_in, ctx_lens, budget: int, recent: int,
@@ -700,6 +712,7 @@ def pa_evict_select(keep, keep_lens, weights_out, weights_in, ctx_lens, budget: 
     [n_seqs, num_heads, budget], ascending, padded with -1); their weights into
     weights_out, which may be weights_in."""
     torch = _torch or _load_torch()
+    here = _here(torch)
     f32, i32 = torch.float32, torch.int32
     n = ctx_lens.shape[0] if n_seqs is None else int(n_seqs)
     _, heads, wl = weights_in.shape
@@ -709,10 +722,12 @@ def pa_evict_select(keep, keep_lens, weights_out, weights_in, ctx_lens, budget: 
         raise ValueError(f"keep is {tuple(keep.shape)}: {heads} heads, {budget} entries expected")
     sums = n * heads * wl
     _check(_lib.pa_evict_select(
-        _arg("keep", keep, i32, n * heads * budget), _arg("keep_lens", keep_lens, i32, n),
-        _arg("weights_out", weights_out, f32, sums), _arg("weights_in", weights_in, f32, sums), wl,
-        _arg("ctx_lens", ctx_lens, i32, n), n, heads, budget, recent,
-        _arg("status", status, i32, 1), _raw_stream(torch, stream)))
+        _arg("keep", keep, i32, n * heads * budget, here),
+        _arg("keep_lens", keep_lens, i32, n, here),
+        _arg("weights_out", weights_out, f32, sums, here),
+        _arg("weights_in", weights_in, f32, sums, here), wl,
+        _arg("ctx_lens", ctx_lens, i32, n, here), n, heads, budget, recent,
+        _arg("status", status, i32, 1, here), _raw_stream(torch, stream)))
 
 
 def pa_compact_kv(k_caches, v_caches, src_tables, dst_tables, src_lens, keep, keep_lens,
@@ -722,6 +737,7 @@ def pa_compact_kv(k_caches, v_caches, src_tables, dst_tables, src_lens, keep, ke
     move to first + j (dst_tables).  keep: int32 [n_seqs, 1 or num_heads, n]
     or [n_seqs, n] (one list for all heads)."""
     torch = _torch or _load_torch()
+    here = _here(torch)
     f16, i32 = torch.float16, torch.int32
     L = len(k_caches)
     n = keep_lens.shape[0] if n_seqs is None else int(n_seqs)
@@ -734,14 +750,14 @@ def pa_compact_kv(k_caches, v_caches, src_tables, dst_tables, src_lens, keep, ke
         raise ValueError("src_tables and dst_tables differ in width")
     c = desc.c
     cache = c.num_blocks * c.block_size * c.num_heads * c.head_dim
-    kp = (ctypes.c_void_p * L)(*[_arg("k_caches", x, f16, cache) for x in k_caches])
-    vp = (ctypes.c_void_p * L)(*[_arg("v_caches", x, f16, cache) for x in v_caches])
+    kp = (ctypes.c_void_p * L)(*[_arg("k_caches", x, f16, cache, here) for x in k_caches])
+    vp = (ctypes.c_void_p * L)(*[_arg("v_caches", x, f16, cache, here) for x in v_caches])
     _check(_lib.pa_compact_kv(
-        kp, vp, L, _arg("src_tables", src_tables, i32, n * mb),
-        _arg("dst_tables", dst_tables, i32, n * mb), _arg("src_lens", src_lens, i32, n),
-        _arg("first", first, i32, n), _arg("keep", keep, i32, n * heads * stride),
-        _arg("keep_lens", keep_lens, i32, n), heads, stride, n, mb, desc.ref,
-        _arg("status", status, i32, 1), _raw_stream(torch, stream)))
+        kp, vp, L, _arg("src_tables", src_tables, i32, n * mb, here),
+        _arg("dst_tables", dst_tables, i32, n * mb, here), _arg("src_lens", src_lens, i32, n, here),
+        _arg("first", first, i32, n, here), _arg("keep", keep, i32, n * heads * stride, here),
+        _arg("keep_lens", keep_lens, i32, n, here), heads, stride, n, mb, desc.ref,
+        _arg("status", status, i32, 1, here), _raw_stream(torch, stream)))
 
 
 def pa_selftest_bounded_wait(status, stream=None) -> None:

@@ -57,6 +57,9 @@ class Fake:
     def is_contiguous(self):
         return self.contiguous
 
+    def dim(self):
+        return len(self.shape)
+
     def numel(self):
         return int(torch.Size(self.shape).numel())
 
@@ -105,3 +108,48 @@ def test_workspaces_are_checked(call, one_gpu):
         call(workspace=Fake((1 << 20,), torch.float32))
     with pytest.raises(pk.PagedKVError, match="workspace"):
         call(workspace=None, scale=0.1)
+
+
+def _verify(**changed):
+    p = Fake((6, 50), torch.float32)
+    a = dict(path=_i32(2, 0), path_lens=_i32(2), next_tokens=_i32(2), target_probs=p, draft_probs=p,
+             draft_tokens=_i32(6), parents=_i32(6), q_starts=_i32(3), u_accept=Fake((6,), torch.float32),
+             u_sample=Fake((2,), torch.float32), stream=0)      # (max_q_len 0)
+    pk.pa_verify_draft(**{**a, **changed})
+
+
+def _select(**changed):
+    w = Fake((2, 2, 64), torch.float32)
+    a = dict(keep=_i32(2, 2, 8), keep_lens=_i32(2), weights_out=w, weights_in=w, ctx_lens=_i32(2),
+             budget=8, recent=9, stream=0)
+    pk.pa_evict_select(**{**a, **changed})
+
+
+def _move(**changed):
+    c = Fake((8, 2, 16, 64))
+    a = dict(k_caches=[c], v_caches=[c], src_tables=_i32(2, 4), dst_tables=_i32(2, 4),
+             src_lens=_i32(2), keep=_i32(2, 8), keep_lens=_i32(2), desc=DESC, first=_i32(2), stream=0)
+    pk.pa_compact_kv(**{**a, **changed})
+
+
+@pytest.mark.parametrize("call,tensors,refusal", [
+    (_tree, {"out": Fake((4, 2, 64), device=1), "q": Fake((4, 2, 64), device=1),
+             "k_cache": Fake((8, 2, 16, 64), device=1), "v_cache": Fake((8, 2, 16, 64), device=1),
+             "block_tables": _i32(2, 4, device=1), "ctx_lens": _i32(2, device=1),
+             "q_starts": _i32(3, device=1), "parents": _i32(4, device=1),
+             "workspace": Fake((1 << 30,), torch.uint8, device=1), "status": _i32(1, device=1)}, "scale"),
+    (_weights, {"out": Fake((2, 2, 64), device=1), "weights_out": Fake((2, 2, 64), torch.float32, device=1),
+                "weights_in": Fake((2, 2, 64), torch.float32, device=1),
+                "workspace": Fake((1 << 30,), torch.uint8, device=1)}, "scale"),
+    (_verify, {"target_probs": Fake((6, 50), torch.float32, device=1), "u_sample": Fake((2,), torch.float32, device=1),
+               "path": _i32(2, 0, device=1)}, "max_q_len"),
+    (_select, {"keep": _i32(2, 2, 8, device=1), "ctx_lens": _i32(2, device=1)}, "recent"),
+    (_move, {"k_caches": [Fake((8, 2, 16, 64), device=1)], "first": _i32(2, device=1),
+             "dst_tables": _i32(2, 4, device=1)}, "overlap")])
+def test_tensors_on_another_gpu_are_refused(call, tensors, refusal, one_gpu):
+    """Kernels run on the current GPU, which all tensors have to be on."""
+    with pytest.raises(pk.PagedKVError, match=refusal):      # nothing else is wrong
+        call()
+    for name, t in tensors.items():
+        with pytest.raises(ValueError, match=name):
+            call(**{name: t})
