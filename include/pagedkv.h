@@ -558,7 +558,12 @@ int pa_tree_attention(void *out, const void *q, const void *k_cache, const void 
                       int32_t *status, const pa_pool_desc *desc, void *stream);
 
 /* Verification of drafted nodes from given uniform numbers, so that the
- * tokens kept are distributed as the target's own samples.  From the root on,
+ * tokens kept are distributed as the target's own samples, provided that each
+ * node's token was drawn from its parent's row of draft_probs, siblings
+ * independently of one another (the same token may come twice), or, with
+ * draft_probs NULL, was picked in any way that does not look at u_accept and
+ * u_sample.  A tree of the drafter's most probable tokens is of the second kind:
+ * pass NULL for it, not the drafter's probabilities.  From the root on,
  * at node v with target probabilities p = target_probs[row of v] and draft
  * probabilities q = draft_probs[row of v], w = p and Z = 1 at first, the
  * children c of v in index order, with token x = draft_tokens[row of c]:
@@ -568,7 +573,11 @@ int pa_tree_attention(void *out, const void *q, const void *k_cache, const void 
  * Where no child is accepted, next_tokens[s] is the first i whose running sum
  * of w passes u_sample[s] * sum w (the last i of positive weight where
  * rounding leaves none), so the call also samples where there is no draft.
- * Evaluated to 2^-48 or better.
+ * Evaluated with pairs of fp32: with W the sum of the node's row of target_probs
+ * and m = 16 for every 131072 tokens begun, sums are off by (m^2 2^-48 + 2^-40) W at
+ * most (2^-39 W for up to 131072 tokens); a rejection at most doubles the error
+ * and adds as much again.  A number that close to a border may fall to its other
+ * side, never to a token without weight.
  *   path          [n_seqs][max_q_len] int32, out: the accepted nodes, the root
  *                 (0) first, ascending, padded with -1
  *   path_lens     [n_seqs] int32, out: how many (>= 1)

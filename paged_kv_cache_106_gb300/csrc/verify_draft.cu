@@ -17,10 +17,16 @@
 // Exactness.  A running sum crosses an edge at every token, so rounding of
 // 2^-24 in it would move the answer once in some hundred samples at 50 k
 // tokens.  All weights and sums are therefore pairs of fp32 (value + error
-// term, 2^-46 or better in all), added with error-free transformations; in
-// fp64 the additions alone would take three times a row's bytes (this GPU does
-// two fp64 operations a clock and SM).  No atomics: the result depends only on
-// the inputs.
+// term), added with error-free transformations; in fp64 the additions alone
+// would take three times a row's bytes (this GPU does two fp64 operations a clock
+// and SM).  What a pair cannot hold, with u = 2^-24 and W the row's sum: after j
+// terms of `plus` the error term is j u W at most and its two roundings 2 j u^2 W,
+// so a lane's m terms of a segment make m^2 u^2 W (m is 16 up to 131072 tokens;
+// in trials it is 2^-46 W for 16 terms, 2^-44 W for 64); each `add` makes 3 u^2 W
+// at most, and there are 5 over the lanes, up to 32 over the segments and some 25
+// over the warps and in the search, 2^-40 W in all.  A rejection is exact the
+// first time and makes some 2^-44 W after that, beside Z's own error.  No atomics:
+// the result depends only on the inputs.
 //
 // What bounds it: the rows it has to read (one target row, and one draft row
 // once something is rejected, 4 V bytes each) for a large batch; the chain of
@@ -38,8 +44,8 @@
 //
 // Measured (in a graph): 256 chains of 5 to 9 nodes, 50272 tokens, fp32 30 us (the
 // rows that have to be read take 15 at 6.78 TB/s); 64 trees of 10 to 26 nodes,
-// 100003 tokens, fp16 60 us (4; two to three passes one after another, and two
-// rows in three begin off the vector boundary); one chain of 8, 32000 tokens,
+// 100003 tokens, fp16 60 us (4; two to three passes one after another, each of
+// which applies all rejections so far to every element); one chain of 8, 32000 tokens,
 // 8.7 us (launch, gather, walk, sum, search: each waits for the one before).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

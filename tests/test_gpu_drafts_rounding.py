@@ -178,3 +178,21 @@ def test_verify_random_numbers_on_a_border(V, front, back, S):
     for us, want in ((0.5 - 2.0 ** -12, range(front)), (0.5 + 2.0 ** -12, [back])):
         _, _, nxt = _verify(_dev(p), None, np.zeros(S), None, starts, np.zeros(S), np.full(S, us), status=st)
         assert np.isin(nxt, list(want)).all()
+
+
+def test_picked_tokens_leave_the_target_its_distribution():
+    """Siblings that are always the drafter's three most probable tokens, without
+    draft probabilities: the token decided after the root has the target's
+    distribution.  40000 draws, 12 tokens: every frequency within 5 standard
+    deviations."""
+    S, V = 40000, 12
+    r = np.random.default_rng(9)
+    p1 = r.dirichlet(np.ones(V))
+    starts = np.arange(S + 1) * 4
+    p = torch.from_numpy(np.tile(p1, (4 * S, 1))).float().cuda()
+    tokens = np.tile(np.array([0, 7, 2, 5], np.int32), S)
+    up = np.tile(np.array([-1, 0, 0, 0], np.int32), S)
+    path, lens, nxt = _verify(p, None, tokens, up, starts, r.random(4 * S), r.random(S))
+    first = np.where(lens > 1, tokens[starts[:-1] + path[:, 1]], nxt)
+    f = np.bincount(first, minlength=V) / S
+    assert (np.abs(f - p1) <= 5 * np.sqrt(p1 * (1 - p1) / S)).all()
