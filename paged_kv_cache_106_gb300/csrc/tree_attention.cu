@@ -61,12 +61,12 @@
 // waits for this one's end (one sequence: 14.2 instead of 14.5 us).
 //
 // Measured (in a graph; share of the bytes' time at 6.78 TB/s): 64 sequences of
-// 128 to 2048, 4 to 16 nodes, 40 heads of 128: 217 us (98 %); 256 sequences of 128
-// to 1536, 64 nodes: 767 us (90 %; the softmax of 64 rows and the end of each
+// 128 to 2048, 4 to 16 nodes, 40 heads of 128: 215 us (98 %); 256 sequences of 128
+// to 1536, 64 nodes: 765 us (91 %; the softmax of 64 rows and the end of each
 // unit, 3.2 of 3.4 thousand clocks a tile, are what bounds it); 3 of 40 to 65
-// thousand, 17 to 31 nodes, 32 heads of 64: 217 us (88 %); 1 of 2048, 8 nodes:
-// 14.1 us against 6.2 (two launches, the plan, one round of loads: latency).
-// Weights form: 64 sequences 221 us (97 %), 2 of 50 to 65 thousand 384 us (92 %).
+// thousand, 17 to 31 nodes, 32 heads of 64: 216 us (88 %); 1 of 2048, 8 nodes:
+// 14.2 us against 6.2 (two launches, the plan, one round of loads: latency).
+// Weights form: 64 sequences 220 us (97 %), 2 of 50 to 65 thousand 381 us (93 %).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>

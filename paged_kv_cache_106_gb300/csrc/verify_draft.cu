@@ -42,11 +42,11 @@
 // CTA goes through it about once, and with everything unrolled its instructions
 // came slower than the data (112 us).
 //
-// Measured (in a graph): 256 chains of 5 to 9 nodes, 50272 tokens, fp32 30 us (the
+// Measured (in a graph): 256 chains of 5 to 9 nodes, 50272 tokens, fp32 31 us (the
 // rows that have to be read take 15 at 6.78 TB/s); 64 trees of 10 to 26 nodes,
-// 100003 tokens, fp16 60 us (4; two to three passes one after another, each of
+// 100003 tokens, fp16 62 us (4; two to three passes one after another, each of
 // which applies all rejections so far to every element); one chain of 8, 32000 tokens,
-// 8.7 us (launch, gather, walk, sum, search: each waits for the one before).
+// 9.0 us (launch, gather, walk, sum, search: each waits for the one before).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
