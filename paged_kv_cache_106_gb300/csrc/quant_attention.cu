@@ -247,6 +247,12 @@ struct Shares {
 __device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A bounded wait whose end is one for the whole warp: lanes see the timer and the
+// status at different moments, and what follows a wait takes all lanes or none.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const int32_t *status) {
+    return __all_sync(kAll, mbar_wait_bounded(bar, parity, status, true));
+}
+
 template <int D>
 __device__ __forceinline__ void store4(const QuantParams &p, int64_t row, int d, float a, float b, float c, float e) {
     const uint2 w = p.bf16 ? make_uint2(quant::pack2<__nv_bfloat16>(a, b), quant::pack2<__nv_bfloat16>(c, e))
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
                     n2 = (ctx2 + TT - 1) >> tshift;
                 } while (n2 == 0);
             }
-            if (seg >= 2) ok = mbar_wait_bounded(smem_addr(q_empty + (seg & 1)), ((seg >> 1) & 1) ^ 1, p.status, true);
+            if (seg >= 2) ok = warp_wait(smem_addr(q_empty + (seg & 1)), ((seg >> 1) & 1) ^ 1, p.status);
             const int64_t from = (int64_t)hg * G * p.rec, step = (int64_t)p.H * p.rec;
             for (int j = 0; j < left && ok; ++j) {
                 const int valid = min(TT, ctx - (tile + j) * TT);
@@ -387,8 +393,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
                 const int now = id;
                 if (j + 1 < left) id = entry(s, ctx, tile + j + 1);
                 else if (issued + 1 < count) id = entry(s2, ctx2, 0);
-                if (round > 0) ok = mbar_wait_bounded(smem_addr(empty + st), (round & 1) ^ 1, p.status, true);
-                ok = __all_sync(kAll, ok);
+                if (round > 0) ok = warp_wait(smem_addr(empty + st), (round & 1) ^ 1, p.status);
                 if (!ok) {
                     report(p.status, PA_ERR_TIMEOUT);
                     break;
@@ -421,7 +426,6 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
             n = n2;
             tile = 0;
         }
-        ok = __all_sync(kAll, ok);
         if (!ok) report(p.status, PA_ERR_TIMEOUT);
         if (!p.by_unit && lane == 0) p.jobs[blockIdx.x] = job;
         // no copy is in flight when the CTA ends
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
 
     bool ok = true;
     for (int done = 0, seg = 0; done < count && ok; ++seg) {
-        ok = mbar_wait_bounded(smem_addr(full + st), phase, p.status, true);   // the stretch's first tile
+        ok = warp_wait(smem_addr(full + st), phase, p.status);   // the stretch's first tile
         if (!ok) break;
         const Stretch m = stretch[seg & 1];
         done += m.tiles;
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
         }
         int valid = m.positions - base;          // from this warp's first position of the tile on
         for (int tile = 0; tile < m.tiles; ++tile, valid -= TT) {
-        if (tile > 0) ok = mbar_wait_bounded(smem_addr(full + st), phase, p.status, true);
+        if (tile > 0) ok = warp_wait(smem_addr(full + st), phase, p.status);
         if (!ok) break;
         const uint32_t at = smem_addr(smem) + st * stage_bytes;
         if (valid > 0 && cols > 0) {
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
             const uint32_t bar = smem_addr(merged + group);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
-            if (!mbar_wait_bounded(bar, merges & 1, p.status, true)) {
+            if (!warp_wait(bar, merges & 1, p.status)) {
                 ok = false;
                 break;
             }
@@ -840,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
             // before anyone writes its share of the next stretch
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
-            if (!mbar_wait_bounded(bar, merges & 1, p.status, true)) {
+            if (!warp_wait(bar, merges & 1, p.status)) {
                 ok = false;
                 break;
             }
