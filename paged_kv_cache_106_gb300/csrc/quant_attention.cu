@@ -361,8 +361,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
         };
         int id = count > 0 ? entry(s, ctx, tile) : -1;
         bool ok = true;
-        for (int seg = 0; issued < count && ok; ++seg) {
-            const int left = min(n - tile, count - issued);     // tiles of this unit
+        // (after a wait that gave up it goes on without copies: the second kernel reads
+        // the entry of every unit that begins here)
+        for (int seg = 0; issued < count; ++seg) {
+            const int left = min(n - tile, count - issued), after = issued + left;     // tiles of this unit
             const bool whole = left == n;
             if (tile == 0) {
                 // (up to the CTA that its last tile is in)
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
                     n2 = (ctx2 + TT - 1) >> tshift;
                 } while (n2 == 0);
             }
-            if (seg >= 2) ok = warp_wait(smem_addr(q_empty + (seg & 1)), ((seg >> 1) & 1) ^ 1, p.status);
+            if (seg >= 2 && ok) ok = warp_wait(smem_addr(q_empty + (seg & 1)), ((seg >> 1) & 1) ^ 1, p.status);
             const int64_t from = (int64_t)hg * G * p.rec, step = (int64_t)p.H * p.rec;
             for (int j = 0; j < left && ok; ++j) {
                 const int valid = min(TT, ctx - (tile + j) * TT);
@@ -420,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
                     ++round;
                 }
             }
+            issued = after;
             s = s2;
             u = u2;
             ctx = ctx2;
@@ -429,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
         if (!ok) report(p.status, PA_ERR_TIMEOUT);
         if (!p.by_unit && lane == 0) p.jobs[blockIdx.x] = job;
         // no copy is in flight when the CTA ends
-        for (int i = max(0, issued - p.stages); i < issued; ++i)
+        const int copied = round * p.stages + st;
+        for (int i = max(0, copied - p.stages); i < copied; ++i)
             if (!mbar_wait_bounded(smem_addr(full + i % p.stages), (i / p.stages) & 1, p.status, false)) {
                 report(p.status, PA_ERR_TIMEOUT);
                 break;

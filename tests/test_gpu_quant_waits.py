@@ -1,7 +1,8 @@
-"""Attention over a quantised cache whose bounded waits give up, without a fault: a
-status word that already holds PA_ERR_TIMEOUT ends every wait that does not
-succeed at once.  Such a call ends, keeps to its own output, and leaves nothing that the
-next call on its workspace meets."""
+"""Attention over a quantised cache whose bounded waits may give up, without a fault:
+with a status word that already holds PA_ERR_TIMEOUT a wait gives up as soon as its
+barrier has not come by the hardware's own limit (which copies rarely exceed, so most
+runs see few or none).  Whichever do, the call ends, keeps to its own output, and
+leaves nothing that the next call on its workspace meets."""
 import time
 
 import numpy as np
@@ -41,3 +42,28 @@ def test_many_sequences(H, rep, D, B, bits):
     for _ in range(3):
         _given_up(b, ws)
         assert torch.equal(b.run(qz.status(), ws=ws), good)
+
+
+@pytest.mark.parametrize("H,rep,D,B,bits,units", [(8, 4, 128, 16, 4, 2), (2, 20, 64, 32, 4, 2), (4, 8, 128, 16, 8, 1),
+                                                  (1, 70, 128, 16, 4, 3)])
+def test_entries_of_few_sequences(H, rep, D, B, bits, units):
+    """Units whose parts are joined by an entry each, several to a CTA: every entry
+    is written (they come first in the workspace: first CTA, parts, sequence, unit, or
+    zeros), whatever stood there, and no other sequence's."""
+    ctx = [60000, 0] + [40] * 60 + [-3, 9000] + [17] * 30
+    b = Batch(H + rep, ctx, H, rep, D, B, bits)
+    good = b.run()
+    ws = torch.empty(pk.pa_decode_quant_workspace_bytes(len(ctx), H * rep, b.desc()), dtype=torch.uint8, device="cuda")
+    want = np.stack(np.divmod(np.arange(len(ctx) * units), units), 1)
+    empty = np.repeat(np.array(ctx) <= 0, units)
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count * 3
+    assert len(want) <= ctas * 2 // 3
+    for before in (-99, 0):
+        ws.view(torch.int32).fill_(before)
+        _given_up(b, ws)
+        entry = ws[:16 * len(want)].view(torch.int32).reshape(-1, 4).cpu().numpy()
+        assert (entry[empty] == 0).all()
+        first, parts = entry[~empty, 0], entry[~empty, 1]
+        assert (entry[~empty, 2:] == want[~empty]).all()
+        assert (first >= 0).all() and (parts >= 1).all() and (first + parts <= ctas).all()
+    assert torch.equal(b.run(qz.status(), ws=ws), good)
