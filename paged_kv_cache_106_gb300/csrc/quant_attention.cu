@@ -74,7 +74,7 @@ struct QuantParams {
     const uint8_t *k, *v;
     const int32_t *tables, *ctx;
     int n_seqs, max_blocks, num_blocks, H, Hq, rep, bshift, rec, bf16;
-    float mult, sign;             // |scale| log2 e, and its sign
+    float scale, sign;            // |scale|, and its sign
     int lg, lqg, lns;             // log2 of a CTA's heads, column groups, shares of a tile's positions
     int head_groups, col_passes;
     int rows;                     // query rows of a unit, at most
@@ -492,9 +492,22 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
             }
 #pragma unroll
             for (int o = 1; o < (PACK ? 4 * GS : 4); o <<= 1) big = max(big, __shfl_xor_sync(kAll, big, o));
-            const int e = min((BITS == 4 ? 2 : -1) - ((int)(big >> 23) - 127), 100);
+            // (a query near either end of bf16's range comes 2^32 nearer to 1 first: every power of
+            // two here then is a normal number, e within -94 .. 104, infinity and NaN aside)
+            const int nearer = big < 32u << 23 ? 32 : big >= 224u << 23 ? -32 : 0;
+            if (nearer != 0) {
+                const float by = __uint_as_float((uint32_t)(127 + nearer) << 23);
+                big = __float_as_uint(__uint_as_float(big) * by);
+#pragma unroll
+                for (int k = 0; k < NG; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[k][j] *= by;
+            }
+            const int e = max(-126, min((BITS == 4 ? 2 : -1) - ((int)(big >> 23) - 127), 104));
             const float up = __uint_as_float((uint32_t)(e + 127) << 23) * p.sign;
-            const float back = query < cols ? p.mult * __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+            // (at most 2^96: a score times it stays finite, and any two that differ are far apart)
+            const float back = query < cols ? fminf(p.scale * __uint_as_float((uint32_t)(127 - e) << 23) *
+                                                        __uint_as_float((uint32_t)(127 - nearer) << 23) * kLog2e, 0x1p96f) : 0.f;
             // (never 0: masked scores are minus infinity before they meet it)
 #pragma unroll
             for (int j = 0; j < NQ; ++j)
@@ -1165,7 +1178,7 @@ int launch_decode_attention_quant(void *out, const void *q, int32_t dtype, int32
     p.bshift = d->block_size == 8 ? 3 : d->block_size == 16 ? 4 : 5;
     p.rec = (int)(block_bytes(d) / d->num_heads);
     p.bf16 = dtype == PA_DTYPE_BF16;
-    p.mult = std::fabs(scale) * kLog2e;
+    p.scale = std::fabs(scale);
     p.sign = scale < 0.f ? -1.f : 1.f;
     p.status = status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
