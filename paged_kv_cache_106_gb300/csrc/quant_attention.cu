@@ -61,6 +61,9 @@ constexpr int kMaxCtas = 1024;                  // of a launch
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                   // a weight may grow to 2^8 before R moves
 constexpr int kLift = 6;                        // scales are lifted below 2^(kLift + 1)
+// Scores (base 2) from here on are rounded to steps that a reference with a lift in it would
+// miss: their maximum is taken off first, the lift comes after.
+constexpr float kFar = 0x1p22f;
 
 // What the copying warp tells the others of a stretch, a unit's tiles that the CTA takes.
 struct Stretch {
@@ -208,6 +211,9 @@ __device__ __forceinline__ void value_pairs(uint32_t a, uint32_t b, uint32_t pic
         p[3] = hadd2(__byte_perm(hi, 0x64646464u, 0x4342), half2_const(0xe480));
     }
 }
+
+// What scales up to these bits are lifted by, as a power of two.
+__device__ __forceinline__ int lift_of(uint32_t bits) { return kLift + 15 - (int)(bits >> 10); }
 
 __device__ __forceinline__ float half_at(uint32_t w, int i) {
     return __half2float(__ushort_as_half((unsigned short)(i ? w >> 16 : w & 0xffffu)));
@@ -469,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
         if (!ok) break;
         const Stretch m = stretch[seg & 1];
         done += m.tiles;
-        uint32_t vref = 0;                       // the largest scale of values, twice
+        uint32_t vref = 0;                       // the largest scale of values, twice; once where a column is beyond kFar
         int cols = 0;
         {
             const int cp = p.col_passes == 1 ? 0 : m.unit % p.col_passes;
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
                 big[j] = fmaxf(x[0][j], x[0][NQ + j]);
 #pragma unroll
                 for (int t = 1; t < MT; ++t) big[j] = fmaxf(big[j], fmaxf(x[t][j], x[t][NQ + j]));
-                big[j] *= mult[j];           // (mult > 0)
+                big[j] = __fmul_rn(big[j], mult[j]);         // (mult > 0)
                 grows |= big[j] > top[j] + kSlack;
             }
             uint32_t v2 = __vmaxu2(vs[0][0][0], vs[0][1][0]);
@@ -664,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
             for (int t = 0; t < MT; ++t)
 #pragma unroll
                 for (int k = t > 0 ? 0 : 1; k < SW; ++k) v2 = __vimax3_u16x2(v2, vs[t][0][k], vs[t][1][k]);
-            // (vref 0: the stretch's first positions)
-            if (__any_sync(kAll, grows || __vmaxu2(v2, vref) != vref || vref == 0)) {
+            // (vref 0: the stretch's first positions; scores beyond kFar come here always)
+            if (__any_sync(kAll, grows || __vmaxu2(v2, vref) != vref || vref < 0x10000u)) {
                 uint32_t vmax = __reduce_max_sync(kAll, max(max(v2 >> 16, v2 & 0xffffu), vref & 0xffffu));
                 // a group that is not finite sets no reference for the others (read again: the words
                 // at hand would cost registers, four grouped heads 112.6 us, so 117.6)
@@ -684,17 +690,34 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
                     }
                     vmax = __reduce_max_sync(kAll, most);
                 }
-                vref = vmax * 0x10001u;
-                const float lift = (float)(kLift + 15 - (int)(vmax >> 10));
+                const float lift = (float)lift_of(vmax), more = (float)(lift_of(vmax) - lift_of(vref & 0xffffu));
                 float f[NQ];
+                bool far = false;
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) big[j] = fmaxf(big[j], __shfl_xor_sync(kAll, big[j], o));
+                    const float was = top[j];
                     top[j] = fmaxf(top[j], big[j]);
-                    f[j] = ex2((lift - top[j]) - R[j]);
-                    R[j] = lift - top[j];
+                    const bool beyond = fabsf(top[j]) >= kFar;
+                    far |= beyond;
+                    f[j] = ex2(beyond || fabsf(was) >= kFar ? (was - top[j]) + more : (lift - top[j]) - R[j]);
+                    R[j] = beyond ? 0.f : lift - top[j];
                     l[j] *= f[j];
+                }
+                far = __any_sync(kAll, far);
+                vref = vmax * (far ? 1u : 0x10001u);
+                if (far) {
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) {
+                        if (!(fabsf(top[j]) >= kFar)) continue;
+                        const float back = 1.f / mult[j];     // (R is 0)
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            x[t][j] = ((__fmul_rn(x[t][j], mult[j]) - top[j]) + lift) * back;
+                            x[t][NQ + j] = ((__fmul_rn(x[t][NQ + j], mult[j]) - top[j]) + lift) * back;
+                        }
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < 2 * GR; ++k)
@@ -755,6 +778,20 @@ __global__ void __launch_bounds__(kThreads, ctas_of(BITS)) quant_attention_kerne
         if (!ok) break;
 
         // ---- the stretch's end
+        if (vref < 0x10000u) {                   // beyond kFar: references without the lift
+            const float down = __uint_as_float((uint32_t)(127 - lift_of(vref & 0xffffu)) << 23);
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                if (!(fabsf(top[j]) >= kFar)) continue;
+                R[j] = -top[j];
+                l[j] *= down;
+#pragma unroll
+                for (int k = 0; k < 2 * GR; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (PACK || (i & 1) == j) O[k][i] *= down;
+            }
+        }
         if constexpr (BITS == 4) {               // dimensions 0 and 2 of four came with 16 times 1 and 3
 #pragma unroll
             for (int k = 0; k < 2 * GR; ++k)
