@@ -845,6 +845,10 @@ def pa_read_kv_quant(k, v, slot_mapping, k_cache, v_cache, desc: PoolDesc, out_s
                              f"tokens of {c.head_dim} expected")
         blocks = k.shape[0]
         rows = blocks * c.block_size
+    elif tuple(k.shape[1:]) != (c.num_heads, c.head_dim):
+        raise ValueError(f"k is {tuple(k.shape)}: rows of {c.num_heads} heads of {c.head_dim} expected")
+    if v is not None and v.__class__ is not int and (v.shape[1:] != k.shape[1:] or v.shape[0] < blocks):
+        raise ValueError(f"v is {tuple(v.shape)}: like k, {tuple(k.shape)}, expected")
     _check(_lib.pa_read_kv_quant(
         _arg("k", k, k.dtype, rows * width, here), _arg("v", v, k.dtype, rows * width, here), kind,
         _arg("slot_mapping", slot_mapping, i64, n, here), _arg("out_slots", out_slots, i64, n, here),
