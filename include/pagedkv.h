@@ -758,7 +758,11 @@ int pa_read_kv_quant(void *k, void *v, int32_t dtype, const int64_t *slot_mappin
  * batches to rounding, not to the bit; it does not depend on where blocks are.
  * Products are of fp16 numbers (codes are exact in fp16; a query is scaled by a power
  * of two, after which its elements below 2^-10 of its largest may be off by 2^-21 of
- * that), sums and softmax statistics fp32; a position's weight times its scale enters the second product
+ * that), sums and softmax statistics fp32.  A score's sums run over codes with a
+ * constant added (1152 in 8 bits, 264 and 24 in turn in 4), which is then taken off, so
+ * their rounding goes by the constant: a score may be off by scale * sum over groups of
+ * s 2^-16 * 1152 (264) * the group's sum of |q|, most of which averages out, and by
+ * 2^-22 of itself.  A position's weight times its scale enters the second product
  * as fp16, an error of 2^-11 of a weight at most (and 2^-31 of the largest weight
  * times the largest finite scale).  The workspace size is 0 where the call would be
  * refused or has nothing to do.
@@ -777,7 +781,9 @@ int pa_decode_attention_quant(void *out, const void *q, int32_t dtype, int32_t q
  *     y = x * (mean(x^2) + eps)^-1/2 * weight      (weight NULL: y = x)
  *     (a, b) -> (a cos - b sin, b cos + a sin) for the rot_dim / 2 pairs of y,
  * pair i being dimensions (i, i + rot_dim / 2), or (2i, 2i + 1) where interleaved;
- * dimensions from rot_dim on are not rotated.  fp32 inside, rounded once.
+ * dimensions from rot_dim on are not rotated.  fp32 inside, rounded once.  The squares
+ * are fp32 too: the norm of a bf16 head wants its largest magnitude below 2^59 and, where
+ * eps is below 2^-100, not below 2^-55.  A head of zeros with a weight and an eps of 0 gives NaN.
  *   q, k          rows of dtype PA_DTYPE_F16 or _BF16, q_heads and kv_heads of
  *                 head_dim a token, with strides as in pa_write_kv_quant; 16-byte
  *                 aligned
