@@ -29,9 +29,10 @@
 // result, at most two a CTA, and a second kernel, launched ahead, joins them.
 //
 // Measured (calls one after another in a graph): 256 sequences of 128 to 4096 positions, 8
-// heads of keys for 64 of queries, 8 bits: 182 us, 6.5 TB/s; 64 of 128 to 2048, 40 heads,
-// 4 bits: 73.8 us, 5.6 TB/s, where the arithmetic on the codes (56 % of the issue slots with
-// twelve warps an SM) no longer hides behind the bytes; one of 2048: 8.8 us, latency.
+// heads of keys for 64 of queries, 8 bits: 181 us, 6.5 TB/s; 64 of 128 to 2048, 40 heads,
+// 4 bits: 74.8 us, 5.5 TB/s, where the arithmetic on the codes (56 % of the issue slots with
+// twelve warps an SM) no longer hides behind the bytes; one of 2048: 9.0 us, latency. The
+// pairs of figures at the choices below are from when each was made.
 #include <cuda_runtime.h>
 
 #include <algorithm>
